@@ -11,6 +11,7 @@ PyTorch is used only for device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -60,6 +61,14 @@ _SIGS = {
     "snack_mse_grad": ([P, P, P, i64, f32, P], ST),
     "snack_gelu_fwd": ([P, P, i64, P], ST),
     "snack_gelu_bwd": ([P, P, P, i64, P], ST),
+    "snack_ckpt_pack": ([P, i64, i64, i32, P, P, P], ST),
+    "snack_ckpt_unpack": ([P, P, i64, i64, i32, P, i32, P], ST),
+    "snack_rmsnorm_fwd": ([P, P, i32, P, f32, i64, i64, P, P, P, i32, P, P, P], ST),
+    "snack_rmsnorm_bwd_work": ([i64, i64, ctypes.POINTER(i64)], ST),
+    "snack_rmsnorm_bwd": ([P, P, i32, P, P, P, P, i64, i64, P, P, P, i64, P], ST),
+    "snack_gelu_ckpt_fwd": ([P, i64, i64, i32, P, P, P, P, P, P], ST),
+    "snack_gelu_ckpt_bwd": ([P, P, P, i64, i64, i32, P, P], ST),
+    "snack_backward_ckpt": ([P, P, P, i32, P, P, P, i32, P], ST),
     "snack_profile_enable": ([ctypes.c_int], ST),
     "snack_profile_reset": ([], ST),
     "snack_profile_name": ([ctypes.c_int], ctypes.c_char_p),
@@ -283,6 +292,58 @@ def snack_gelu_bwd(X, dY, dX, stream=None):
     _check(_lib.snack_gelu_bwd(_ptr(X), _ptr(dY), _ptr(dX), X.numel(), _stream(stream)), "snack_gelu_bwd")
 
 
+F32, BF16, INT8, E4M3 = 0, 1, 2, 3
+
+
+def snack_ckpt_pack(X, fmt, Q, S, stream=None):
+    rows, n = X.shape
+    _check(_lib.snack_ckpt_pack(_ptr(X), rows, n, fmt, _ptr(Q), _ptr(S), _stream(stream)), "snack_ckpt_pack")
+
+
+def snack_ckpt_unpack(Q, S, fmt, Y, y_fmt, stream=None):
+    rows, n = Y.shape
+    _check(_lib.snack_ckpt_unpack(_ptr(Q), _ptr(S), rows, n, fmt, _ptr(Y), y_fmt, _stream(stream)),
+           "snack_ckpt_unpack")
+
+
+def snack_rmsnorm_fwd(X, R, h_fmt, gain, eps, H, Y, rstd, q_fmt=F32, Q=None, S=None, stream=None):
+    rows, n = X.shape
+    _check(_lib.snack_rmsnorm_fwd(_ptr(X), _ptr(R), h_fmt, _ptr(gain), eps, rows, n, _ptr(H), _ptr(Y), _ptr(rstd),
+                                  q_fmt, _ptr(Q), _ptr(S), _stream(stream)), "snack_rmsnorm_fwd")
+
+
+def snack_rmsnorm_bwd_work(rows, n):
+    b = i64()
+    _check(_lib.snack_rmsnorm_bwd_work(rows, n, ctypes.byref(b)), "snack_rmsnorm_bwd_work")
+    return b.value
+
+
+def snack_rmsnorm_bwd(H, HS, h_fmt, gain, rstd, dY, dR, dX, dgain, work, stream=None):
+    """work: a device tensor of at least snack_rmsnorm_bwd_work bytes, or None."""
+    rows, n = dY.shape
+    nbytes = 0 if work is None else work.numel() * work.element_size()
+    _check(_lib.snack_rmsnorm_bwd(_ptr(H), _ptr(HS), h_fmt, _ptr(gain), _ptr(rstd), _ptr(dY), _ptr(dR), rows, n,
+                                  _ptr(dX), _ptr(dgain), _ptr(work), nbytes, _stream(stream)), "snack_rmsnorm_bwd")
+
+
+def snack_gelu_ckpt_fwd(X, fmt, Y, QX=None, SX=None, QY=None, SY=None, stream=None):
+    rows, n = X.shape
+    _check(_lib.snack_gelu_ckpt_fwd(_ptr(X), rows, n, fmt, _ptr(Y), _ptr(QX), _ptr(SX), _ptr(QY), _ptr(SY),
+                                    _stream(stream)), "snack_gelu_ckpt_fwd")
+
+
+def snack_gelu_ckpt_bwd(QX, SX, fmt, dY, dX, stream=None):
+    rows, n = dY.shape
+    _check(_lib.snack_gelu_ckpt_bwd(_ptr(QX), _ptr(SX), _ptr(dY), rows, n, fmt, _ptr(dX), _stream(stream)),
+           "snack_gelu_ckpt_bwd")
+
+
+def snack_backward_ckpt(h, Q, S, fmt, dY, dX=None, dW=None, stream=None):
+    B = dY.shape[0]
+    _check(_lib.snack_backward_ckpt(h, _ptr(Q), _ptr(S), fmt, _ptr(dY), _ptr(dX), _ptr(dW), B, _stream(stream)),
+           "snack_backward_ckpt")
+
+
 def snack_profile_enable(on=True):
     _check(_lib.snack_profile_enable(1 if on else 0), "snack_profile_enable")
 
@@ -335,6 +396,178 @@ def profile_snapshot():
 
 
 # ---------------------------------------------------------------------------
+# Activation checkpoints, the norm and the GELU (tensors made by the call)
+# ---------------------------------------------------------------------------
+
+_HIDDEN = {torch.float32: F32, torch.bfloat16: BF16}
+_BLOCK = 32   # features of a row that share one exponent byte
+
+
+def _on(stream):
+    """Tensors made inside belong to the stream the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _like(t, shape, name, ref, dtype=torch.float32):
+    """t is a contiguous tensor of this dtype and shape on ref's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device != ref.device:
+        raise ValueError(f"{name} must be on the same GPU as the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _matrix(t, name, dtype=torch.float32):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [rows, features], got {tuple(t.shape)}")
+    _like(t, t.shape, name, t, dtype)
+    return t.shape
+
+
+def _kept_format(fmt):
+    if fmt not in (INT8, E4M3):
+        raise ValueError("a checkpoint's format is INT8 or E4M3")
+
+
+class Ckpt:
+    """An activation [rows, n] kept in 8 bits: codes q [rows, 32 ceil(n / 32)] and one exponent byte for every
+    32 features of a row, s [rows, ceil(n / 32)] (uint8 device tensors); a code c stands for c * 2^(s - 127), c a
+    signed integer (INT8) or an e4m3 number (E4M3).  33/32 bytes a value."""
+
+    __slots__ = ("q", "s", "fmt", "n")
+
+    def __init__(self, q, s, fmt, n):
+        _kept_format(fmt)
+        n = int(n)
+        if n < 1:
+            raise ValueError("a checkpoint has at least one feature")
+        nb = -(-n // _BLOCK)
+        rows = _matrix(q, "q", torch.uint8)[0]
+        _like(q, (rows, _BLOCK * nb), "q", q, torch.uint8)
+        _like(s, (rows, nb), "s", q, torch.uint8)
+        self.q, self.s, self.fmt, self.n = q, s, fmt, n
+
+    @classmethod
+    def empty(cls, rows, n, fmt, device):
+        """Room for a checkpoint, on the current stream."""
+        _kept_format(fmt)
+        nb = -(-n // _BLOCK)
+        ck = cls.__new__(cls)
+        ck.q = torch.empty((rows, _BLOCK * nb), dtype=torch.uint8, device=device)
+        ck.s = torch.empty((rows, nb), dtype=torch.uint8, device=device)
+        ck.fmt, ck.n = fmt, n
+        return ck
+
+    @classmethod
+    def pack(cls, x, fmt, stream=None):
+        """The checkpoint of x, float32 [rows, n]."""
+        rows, n = _matrix(x, "x")
+        with _on(stream):
+            ck = cls.empty(rows, n, fmt, x.device)
+        snack_ckpt_pack(x, fmt, ck.q, ck.s, stream)
+        return ck
+
+    def unpack(self, dtype=torch.float32, stream=None):
+        """The values it stands for, in float32 or bfloat16."""
+        if dtype not in _HIDDEN:
+            raise TypeError("a checkpoint is read as float32 or bfloat16")
+        with _on(stream):
+            y = torch.empty((self.rows, self.n), dtype=dtype, device=self.q.device)
+        snack_ckpt_unpack(self.q, self.s, self.fmt, y, _HIDDEN[dtype], stream)
+        return y
+
+    @property
+    def rows(self):
+        return self.q.shape[0]
+
+    @property
+    def nbytes(self):
+        return self.q.numel() + self.s.numel()
+
+
+def rmsnorm_fwd(x, gain, eps, residual=None, q_format=None, want_y=True, stream=None):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain over the rows of x, float32 [rows, n].
+
+    residual: float32 or bfloat16 [rows, n]; h has its type (None: h is x itself).  q_format: INT8 or E4M3 also
+    leaves y's checkpoint; with want_y=False only that.  Returns (h, y, rstd, checkpoint), None where there is none."""
+    rows, n = _matrix(x, "x")
+    _like(gain, (n,), "gain", x)
+    if not want_y and q_format is None:
+        raise ValueError("neither y nor its checkpoint is wanted")
+    h_fmt, h, y, ck = F32, None, None, None
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor) or residual.dtype not in _HIDDEN:
+            raise TypeError("residual must be a float32 or bfloat16 tensor")
+        _like(residual, x.shape, "residual", x, residual.dtype)
+        h_fmt = _HIDDEN[residual.dtype]
+    with _on(stream):
+        if residual is not None:
+            h = torch.empty_like(residual)
+        if want_y:
+            y = torch.empty_like(x)
+        rstd = x.new_empty((rows,))
+        if q_format is not None:
+            ck = Ckpt.empty(rows, n, q_format, x.device)
+    snack_rmsnorm_fwd(x, residual, h_fmt, gain, eps, h, y, rstd, F32 if ck is None else ck.fmt,
+                      None if ck is None else ck.q, None if ck is None else ck.s, stream)
+    return (x if h is None else h), y, rstd, ck
+
+
+def rmsnorm_bwd(h, gain, rstd, dY, dR=None, want_dgain=True, stream=None):
+    """The gradient of rmsnorm_fwd: h as float32 or bfloat16 [rows, n] or as a Ckpt, rstd the forward's, dY float32,
+    dR the gradient that reaches h along the residual stream (None: none).  Returns (dX, dgain): dX is the gradient
+    of both x and residual, dgain None where it is not wanted."""
+    rows, n = _matrix(dY, "dY")
+    if isinstance(h, Ckpt):
+        if (h.rows, h.n) != (rows, n):
+            raise ValueError(f"h must have shape {(rows, n)}, got {(h.rows, h.n)}")
+        if h.q.device != dY.device:
+            raise ValueError("h must be on the same GPU as the other tensors")
+        H, HS, fmt = h.q, h.s, h.fmt
+    else:
+        if not isinstance(h, torch.Tensor) or h.dtype not in _HIDDEN:
+            raise TypeError("h must be a float32 or bfloat16 tensor or a Ckpt")
+        _like(h, dY.shape, "h", dY, h.dtype)
+        H, HS, fmt = h, None, _HIDDEN[h.dtype]
+    _like(gain, (n,), "gain", dY)
+    _like(rstd, (rows,), "rstd", dY)
+    if dR is not None:
+        _like(dR, dY.shape, "dR", dY)
+    with _on(stream):
+        dX = torch.empty_like(dY)
+        dgain = dY.new_empty((n,)) if want_dgain else None
+        work = torch.empty(snack_rmsnorm_bwd_work(rows, n), dtype=torch.uint8, device=dY.device)
+    snack_rmsnorm_bwd(H, HS, fmt, gain, rstd, dY, dR, dX, dgain, work, stream)
+    return dX, dgain
+
+
+def gelu_ckpt_fwd(x, fmt, want_y=True, stream=None):
+    """Exact GELU of x, float32 [rows, n].  Returns (y, checkpoint of x, checkpoint of y)."""
+    rows, n = _matrix(x, "x")
+    with _on(stream):
+        y = torch.empty_like(x) if want_y else None
+        cx, cy = Ckpt.empty(rows, n, fmt, x.device), Ckpt.empty(rows, n, fmt, x.device)
+    snack_gelu_ckpt_fwd(x, fmt, y, cx.q, cx.s, cy.q, cy.s, stream)
+    return y, cx, cy
+
+
+def gelu_ckpt_bwd(ck, dY, stream=None):
+    """dY (Phi(x) + x phi(x)) with x read from its checkpoint; dY float32 [rows, n]."""
+    _like(dY, (ck.rows, ck.n), "dY", ck.q)
+    with _on(stream):
+        dX = torch.empty_like(dY)
+    snack_gelu_ckpt_bwd(ck.q, ck.s, ck.fmt, dY, dX, stream)
+    return dX
+
+
+# ---------------------------------------------------------------------------
 # Convenience object over the same calls
 # ---------------------------------------------------------------------------
 
@@ -375,6 +608,24 @@ class SnackLayer:
             dW = torch.empty((self.nnz,), dtype=torch.float32, device=dY.device)
         snack_backward(self.h, X, dY, dX if want_dx else None, dW if want_dw else None, stream)
         return (dX if want_dx else None), (dW if want_dw else None)
+
+    def backward_ckpt(self, ck, dY, want_dx=True, want_dw=True, dX=None, dW=None, stream=None):
+        """backward() with its input read from a checkpoint (Ckpt of [B, K]); returns (dX, dW)."""
+        _like(dY, (ck.rows, self.M), "dY", ck.q)
+        if ck.n != self.K:
+            raise ValueError(f"the checkpoint must have {self.K} features, got {ck.n}")
+        with _on(stream):
+            if want_dx and dX is None:
+                dX = dY.new_empty((ck.rows, self.K))
+            if want_dw and dW is None:
+                dW = dY.new_empty((self.nnz,))
+        dX, dW = (dX if want_dx else None), (dW if want_dw else None)
+        if dX is not None:
+            _like(dX, (ck.rows, self.K), "dX", ck.q)
+        if dW is not None:
+            _like(dW, (self.nnz,), "dW", ck.q)
+        snack_backward_ckpt(self.h, ck.q, ck.s, ck.fmt, dY, dX, dW if self.nnz else None, stream)
+        return dX, dW
 
     def backward_sgd(self, X, dY, lr, want_dx=True, dX=None, dW=None, stream=None):
         import torch

@@ -33,6 +33,8 @@ enum KernelClass : int {
     KC_SORT,
     KC_CANON,
     KC_PRUNE,
+    KC_CKPT,
+    KC_NORM,
     KC_COUNT
 };
 
@@ -238,6 +240,10 @@ BatchPlan plan_batch(int B);
 // second pair (src2 may be null) is transposed by the same launch
 snack_status transpose_pad(const float* src, float* dst, int n, const float* src2, float* dst2, int n2, int B,
                            int bp, hipStream_t s);
+
+// The same copy from a checkpoint (codes Q, exponent bytes S) of src [B, n] (ckpt.hip)
+snack_status ckpt_transpose(const uint8_t* Q, const uint8_t* S, int fmt, int n, int B, int bp, float* xt,
+                            hipStream_t s);
 
 // Whether every kernel of a forward (fwd) or backward (dx, dw requested) pass
 // can take the caller's batch-major [B][n] arrays directly, so no

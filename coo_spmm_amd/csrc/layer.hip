@@ -409,6 +409,26 @@ extern "C" snack_status snack_backward(snack_layer* L, const float* X, const flo
     return backward_impl(L, X, dY, dX, dW, B, as_stream(stream), nullptr);
 }
 
+extern "C" snack_status snack_backward_ckpt(snack_layer* L, const uint8_t* Q, const uint8_t* S, int32_t fmt,
+                                            const float* dY, float* dX, float* dW, int32_t B, snack_stream stream)
+{
+    if (!L || !Q || !S || !dY || B < 1 || (fmt != SNACK_INT8 && fmt != SNACK_E4M3)) return SNACK_ERR_INVALID_ARG;
+    if (B > kMaxBatch) return SNACK_ERR_UNSUPPORTED;
+    if ((((uintptr_t)dW | (uintptr_t)Q) & 15) != 0) return SNACK_ERR_INVALID_ARG;
+    if (!dX && !dW) return SNACK_OK;
+    hipStream_t s = as_stream(stream);
+    if (!dW) return backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr);
+    const BatchPlan p = plan_batch(B);
+    SNACK_CHECK(ws_check(L, p));
+    // X as the passes of this plan read it, in the workspace's place for its feature-major copy
+    if (p.bp == 1 || spmm_batch_major(L, p, false, dX != nullptr, true)) {
+        SNACK_CHECK(snack_ckpt_unpack(Q, S, B, L->K, fmt, ws_x(L), SNACK_F32, stream));
+        return backward_impl(L, ws_x(L), dY, dX, dW, B, s, nullptr);
+    }
+    SNACK_CHECK(ckpt_transpose(Q, S, fmt, L->K, B, p.bp, ws_x(L), s));
+    return backward_impl(L, ws_x(L), dY, dX, dW, B, s, nullptr, true);
+}
+
 namespace {
 
 // snack_backward_sgd after its argument checks

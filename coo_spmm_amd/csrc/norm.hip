@@ -1,0 +1,479 @@
+// norm.hip -- root-mean-square norm over rows with the residual's addition, its
+// output's 8-bit checkpoint, and its gradient from a hidden state held in fp32,
+// bf16 or as a checkpoint.
+//
+//   h = x + residual (rounded to the residual stream's type)
+//   y = h rstd gain,  rstd = 1 / sqrt(mean(h^2) + eps)
+//   dx = rstd (w - xh mean(w xh)) + dR,  xh = h rstd,  w = dY gain
+//   dgain = sum over rows of dY xh
+//
+// Both directions are one pass over HBM: a row stays in registers between its
+// sum and its outputs.  Rows of up to 1024 features take one wavefront each
+// (the sum never leaves it), longer ones a workgroup of as many wavefronts as
+// give every thread at most four groups of four features; rows past 16384
+// features, which no longer fit, are read twice.  Features are dealt to threads
+// so that eight neighbouring lanes always hold one 32-feature block.
+// dgain: every workgroup adds up its own rows' terms in registers, in row order,
+// and writes one row of partial sums; a second kernel adds the partial rows in a
+// fixed tree.  No atomics, so the result does not depend on timing.
+#include "ckpt.h"
+
+namespace snack {
+namespace {
+
+constexpr int kChunks = 4;                       // groups of four features a thread holds
+constexpr int kWaveRow = kWave * 4 * kChunks;    // longest row of one wavefront
+constexpr int kRowMax = 1024 * 4 * kChunks;      // longest row of one workgroup
+constexpr int kLongThreads = 1024;               // workgroup of the rows past it
+constexpr int kBwdGroups = 512;                  // most workgroups (and partial rows) of the gradient
+constexpr int kColThreads = 256;                 // column pass of rows past kRowMax
+constexpr int kSumCols = 32, kSumRows = 32;      // final sum: columns and row strides of a workgroup
+
+// x added over the lanes of a wavefront, the same tree in every lane
+__device__ inline float wave_sum(float x)
+{
+#pragma unroll
+    for (int m = kWave / 2; m >= 1; m >>= 1) x += __shfl_xor(x, m, kWave);
+    return x;
+}
+
+// the same over a workgroup; part holds 16 floats.  Every thread gets the sum;
+// safe to call again at once with the other half of a doubled buffer
+__device__ inline float group_sum(float x, float* part)
+{
+    x = wave_sum(x);
+    const int w = (int)threadIdx.x / kWave, nw = (int)blockDim.x / kWave;
+    if ((threadIdx.x & (kWave - 1)) == 0) part[w] = x;
+    __syncthreads();
+    float s = 0.0f;
+    for (int i = 0; i < nw; ++i) s += part[i];
+    return s;
+}
+
+template <int HF>
+struct HType { using T = float; };
+template <>
+struct HType<SNACK_BF16> { using T = uint16_t; };
+
+__device__ inline f32x4 load4(const float* __restrict__ p, int64_t left)
+{
+    if (left >= 4) return *reinterpret_cast<const f32x4u*>(p);
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (left > 0) v.x = p[0];
+    if (left > 1) v.y = p[1];
+    if (left > 2) v.z = p[2];
+    return v;
+}
+__device__ inline f32x4 load4(const uint16_t* __restrict__ p, int64_t left)
+{
+    u16x4u h = {0, 0, 0, 0};
+    if (left >= 4) {
+        h = *reinterpret_cast<const u16x4u*>(p);
+    } else {
+        if (left > 0) h.x = p[0];
+        if (left > 1) h.y = p[1];
+        if (left > 2) h.z = p[2];
+    }
+    return f32x4{bf16_value(h.x), bf16_value(h.y), bf16_value(h.z), bf16_value(h.w)};
+}
+__device__ inline void store4(float* __restrict__ p, f32x4 v, int64_t left)
+{
+    if (left >= 4) {
+        *reinterpret_cast<f32x4u*>(p) = v;
+        return;
+    }
+    if (left > 0) p[0] = v.x;
+    if (left > 1) p[1] = v.y;
+    if (left > 2) p[2] = v.z;
+}
+__device__ inline void store4(uint16_t* __restrict__ p, f32x4 v, int64_t left)
+{
+    const u16x4u h = {bf16_bits(v.x), bf16_bits(v.y), bf16_bits(v.z), bf16_bits(v.w)};
+    if (left >= 4) {
+        *reinterpret_cast<u16x4u*>(p) = h;
+        return;
+    }
+    if (left > 0) p[0] = h.x;
+    if (left > 1) p[1] = h.y;
+    if (left > 2) p[2] = h.z;
+}
+__device__ inline float dot4(f32x4 a, f32x4 b) { return fmaf(a.x, b.x, a.y * b.y) + fmaf(a.z, b.z, a.w * b.w); }
+
+struct FwdArgs {
+    const float* X;
+    const void* R;       // residual, or null
+    const float* gain;
+    void* H;             // h, or null (no residual: h is X)
+    float* Y;            // or null
+    float* rstd;
+    uint8_t* Q;          // checkpoint of y, or null
+    uint8_t* S;
+    int64_t rows, n, per_row;   // per_row: blocks of a row
+    float eps;
+};
+
+// h of four features: x + residual, rounded to the stream's type
+template <int HF>
+__device__ inline f32x4 hidden4(const FwdArgs& A, int64_t at, int64_t left)
+{
+    f32x4 h = load4(A.X + at, left);
+    if (A.R) {
+        h += load4(reinterpret_cast<const typename HType<HF>::T*>(A.R) + at, left);
+        if constexpr (HF == SNACK_BF16)
+            h = f32x4{bf16_value(bf16_bits(h.x)), bf16_value(bf16_bits(h.y)), bf16_value(bf16_bits(h.z)),
+                      bf16_value(bf16_bits(h.w))};
+    }
+    return h;
+}
+
+// y of four features and what is kept of it
+template <int QF>
+__device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t at, int64_t left, f32x4 h, float r)
+{
+    const f32x4 y = h * r * load4(A.gain + f, left);
+    if (A.Y) store4(A.Y + at, y, left);
+    if constexpr (QF != SNACK_F32) {
+        const int64_t blk = row * A.per_row + f / kCkptBlock;
+        ckpt_store<QF>(y, (uint32_t*)(A.Q + blk * kCkptBlock) + ((f / 4) & 7), A.S + blk, (int)((f / 4) & 7));
+    }
+}
+
+// WG: a workgroup a row; else a wavefront a row
+template <int HF, int QF, bool WG>
+__global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
+{
+    __shared__ float part[16];
+    using T = typename HType<HF>::T;
+    const int64_t row = WG ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+    if (row >= A.rows) return;   // never with WG
+    const int t = WG ? (int)threadIdx.x : (int)threadIdx.x & (kWave - 1);
+    const int nt = WG ? (int)blockDim.x : kWave;
+    const int64_t base = row * A.n;
+    f32x4 h[kChunks];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int64_t f = 4 * (t + (int64_t)i * nt);
+        h[i] = hidden4<HF>(A, base + f, A.n - f);
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int64_t f = 4 * (t + (int64_t)i * nt);
+        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h[i], A.n - f);
+        ss += dot4(h[i], h[i]);
+    }
+    ss = WG ? group_sum(ss, part) : wave_sum(ss);
+    const float r = 1.0f / sqrtf(ss / (float)A.n + A.eps);
+    if (t == 0) A.rstd[row] = r;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int64_t f = 4 * (t + (int64_t)i * nt);
+        // whole blocks: the eight lanes of a row's last block stay together
+        if ((f & ~(int64_t)(kCkptBlock - 1)) < A.n) finish4<QF>(A, row, f, base + f, A.n - f, h[i], r);
+    }
+}
+
+// rows past kRowMax: h made twice
+template <int HF, int QF>
+__global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(FwdArgs A)
+{
+    __shared__ float part[16];
+    using T = typename HType<HF>::T;
+    const int64_t row = blockIdx.x, base = row * A.n;
+    float ss = 0.0f;
+    for (int64_t f = 4 * (int64_t)threadIdx.x; f < A.n; f += 4 * kLongThreads) {
+        const f32x4 h = hidden4<HF>(A, base + f, A.n - f);
+        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h, A.n - f);
+        ss += dot4(h, h);
+    }
+    ss = group_sum(ss, part);
+    const float r = 1.0f / sqrtf(ss / (float)A.n + A.eps);
+    if (threadIdx.x == 0) A.rstd[row] = r;
+    for (int64_t f = 4 * (int64_t)threadIdx.x; (f & ~(int64_t)(kCkptBlock - 1)) < A.n; f += 4 * kLongThreads)
+        finish4<QF>(A, row, f, base + f, A.n - f, hidden4<HF>(A, base + f, A.n - f), r);
+}
+
+struct BwdArgs {
+    const void* H;        // h: fp32, bf16, or the codes of a checkpoint
+    const uint8_t* HS;    // the checkpoint's exponent bytes
+    const float* gain;
+    const float* rstd;
+    const float* dY;
+    const float* dR;      // gradient that reaches h directly, or null
+    float* dX;
+    float* part;          // [gridDim.x][n] partial sums of dgain, or null
+    float* mean;          // [rows] mean(w xh) (rows past kRowMax)
+    int64_t rows, n, per_row;
+};
+
+template <int HF>
+__device__ inline f32x4 kept4(const BwdArgs& A, int64_t row, int64_t f, int64_t left)
+{
+    if constexpr (HF == SNACK_INT8 || HF == SNACK_E4M3) {
+        if (left <= 0) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int64_t blk = row * A.per_row + f / kCkptBlock;
+        const uint32_t w = ((const uint32_t*)A.H)[blk * (kCkptBlock / 4) + ((f / 4) & 7)];
+        f32x4 v = ckpt_codes4<HF>(w) * ckpt_scale(A.HS[blk]);
+        // codes past the row's end are not values
+        if (left < 2) v.y = 0.0f;
+        if (left < 3) v.z = 0.0f;
+        if (left < 4) v.w = 0.0f;
+        return v;
+    } else {
+        return load4(reinterpret_cast<const typename HType<HF>::T*>(A.H) + row * A.n + f, left);
+    }
+}
+
+template <int HF, bool WG>
+__global__ void __launch_bounds__(WG ? 1024 : 256) norm_bwd_kernel(BwdArgs A)
+{
+    __shared__ float part[32];
+    __shared__ float gsum[WG ? 1 : 3 * kWaveRow];
+    const int wave = (int)threadIdx.x / kWave;
+    const int t = WG ? (int)threadIdx.x : (int)threadIdx.x & (kWave - 1);
+    const int nt = WG ? (int)blockDim.x : kWave;
+    const int64_t step = WG ? (int64_t)gridDim.x : (int64_t)gridDim.x * 4;
+    const float inv_n = 1.0f / (float)A.n;
+    f32x4 g[kChunks], acc[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int64_t f = 4 * (t + (int64_t)i * nt);
+        g[i] = load4(A.gain + f, A.n - f);
+        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    int flip = 0;
+    for (int64_t row = WG ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave; row < A.rows; row += step) {
+        const float r = A.rstd[row];
+        const int64_t base = row * A.n;
+        f32x4 xh[kChunks], w[kChunks];
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int64_t f = 4 * (t + (int64_t)i * nt);
+            xh[i] = kept4<HF>(A, row, f, A.n - f);
+            w[i] = load4(A.dY + base + f, A.n - f);
+        }
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            xh[i] *= r;
+            acc[i] += w[i] * xh[i];
+            w[i] *= g[i];
+            dot += dot4(w[i], xh[i]);
+        }
+        dot = WG ? group_sum(dot, part + 16 * flip) : wave_sum(dot);
+        flip ^= 1;   // the next row's sums go to the other half, so one barrier a row is enough
+        const float c = dot * inv_n;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int64_t f = 4 * (t + (int64_t)i * nt);
+            f32x4 o = (w[i] - xh[i] * c) * r;
+            if (A.dR) o += load4(A.dR + base + f, A.n - f);
+            store4(A.dX + base + f, o, A.n - f);
+        }
+    }
+    if (!A.part) return;
+    if constexpr (!WG) {
+        // the workgroup's four wavefronts hold the same features: added in wavefront order
+        if (wave > 0) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+                *reinterpret_cast<f32x4*>(&gsum[(wave - 1) * kWaveRow + 4 * (t + i * kWave)]) = acc[i];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+            for (int v = 0; v < 3; ++v)
+                acc[i] += *reinterpret_cast<const f32x4*>(&gsum[v * kWaveRow + 4 * (t + i * kWave)]);
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int64_t f = 4 * (t + (int64_t)i * nt);
+        store4(A.part + (int64_t)blockIdx.x * A.n + f, acc[i], A.n - f);
+    }
+}
+
+// rows past kRowMax, first pass: mean(w xh) of each row
+template <int HF>
+__global__ void __launch_bounds__(kLongThreads) norm_bwd_mean_kernel(BwdArgs A)
+{
+    __shared__ float part[16];
+    const int64_t row = blockIdx.x, base = row * A.n;
+    const float r = A.rstd[row];
+    float dot = 0.0f;
+    for (int64_t f = 4 * (int64_t)threadIdx.x; f < A.n; f += 4 * kLongThreads)
+        dot += dot4(load4(A.dY + base + f, A.n - f) * load4(A.gain + f, A.n - f), kept4<HF>(A, row, f, A.n - f) * r);
+    dot = group_sum(dot, part);
+    if (threadIdx.x == 0) A.mean[row] = dot / (float)A.n;
+}
+
+// second pass: a workgroup takes 1024 columns (blockIdx.y) of rows blockIdx.x, + gridDim.x, ...
+template <int HF>
+__global__ void __launch_bounds__(kColThreads) norm_bwd_cols_kernel(BwdArgs A)
+{
+    const int64_t f = 4 * ((int64_t)blockIdx.y * kColThreads + threadIdx.x);
+    const int64_t left = A.n - f;
+    if (left <= 0) return;
+    const f32x4 g = load4(A.gain + f, left);
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
+        const float r = A.rstd[row], c = A.mean[row];
+        const int64_t at = row * A.n + f;
+        const f32x4 xh = kept4<HF>(A, row, f, left) * r, d = load4(A.dY + at, left);
+        acc += d * xh;
+        f32x4 o = (d * g - xh * c) * r;
+        if (A.dR) o += load4(A.dR + at, left);
+        store4(A.dX + at, o, left);
+    }
+    if (A.part) store4(A.part + (int64_t)blockIdx.x * A.n + f, acc, left);
+}
+
+// out[c] = sum of part[g][c]: 32 strided runs of rows, then the runs in order
+__global__ void __launch_bounds__(kSumCols * kSumRows) part_sum_kernel(const float* __restrict__ part, int groups,
+                                                                       int64_t n, float* __restrict__ out)
+{
+    __shared__ float sh[kSumRows][kSumCols + 1];
+    const int tx = (int)threadIdx.x % kSumCols, ty = (int)threadIdx.x / kSumCols;
+    const int64_t c = (int64_t)blockIdx.x * kSumCols + tx;
+    float a = 0.0f;
+    if (c < n) {
+#pragma unroll 8
+        for (int g = ty; g < groups; g += kSumRows) a += part[(int64_t)g * n + c];
+    }
+    sh[ty][tx] = a;
+    __syncthreads();
+    if (ty == 0 && c < n) {
+        for (int i = 1; i < kSumRows; ++i) a += sh[i][tx];
+        out[c] = a;
+    }
+}
+
+// threads of a workgroup that takes a row of n features (kWaveRow < n <= kRowMax)
+int row_threads(int64_t n) { return kWave * (int)((n + kWaveRow - 1) / kWaveRow); }
+
+// workgroups of the gradient, one partial row of dgain each.  A fixed count (two
+// a CU) rather than one a row: at 3333 x 4999 the partial rows are then a
+// seventh of dY's bytes instead of all of them.
+int bwd_groups(int64_t rows, int64_t n)
+{
+    const int64_t g = n <= kWaveRow ? (rows + 3) / 4 : rows;
+    return (int)(g < kBwdGroups ? g : kBwdGroups);
+}
+
+bool bad_size(int64_t rows, int64_t n) { return n >= (1ll << 31) - kCkptBlock || rows >= (1ll << 31); }
+inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+template <int HF, int QF>
+void launch_fwd(const FwdArgs& A, hipStream_t s)
+{
+    if (A.n <= kWaveRow)
+        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, false>), dim3((unsigned)((A.rows + 3) / 4)), dim3(256), 0, s, A);
+    else if (A.n <= kRowMax)
+        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, true>), dim3((unsigned)A.rows), dim3(row_threads(A.n)), 0, s, A);
+    else
+        hipLaunchKernelGGL((norm_fwd_long_kernel<HF, QF>), dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
+}
+template <int HF>
+void launch_fwd(const FwdArgs& A, int q_fmt, hipStream_t s)
+{
+    if (q_fmt == SNACK_INT8) launch_fwd<HF, SNACK_INT8>(A, s);
+    else if (q_fmt == SNACK_E4M3) launch_fwd<HF, SNACK_E4M3>(A, s);
+    else launch_fwd<HF, SNACK_F32>(A, s);
+}
+
+template <int HF>
+void launch_bwd(const BwdArgs& A, int groups, hipStream_t s)
+{
+    if (A.n <= kWaveRow) {
+        hipLaunchKernelGGL((norm_bwd_kernel<HF, false>), dim3((unsigned)groups), dim3(256), 0, s, A);
+    } else if (A.n <= kRowMax) {
+        hipLaunchKernelGGL((norm_bwd_kernel<HF, true>), dim3((unsigned)groups), dim3(row_threads(A.n)), 0, s, A);
+    } else {
+        hipLaunchKernelGGL(norm_bwd_mean_kernel<HF>, dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
+        const unsigned cols = (unsigned)((A.n + 4 * kColThreads - 1) / (4 * kColThreads));
+        hipLaunchKernelGGL(norm_bwd_cols_kernel<HF>, dim3((unsigned)groups, cols), dim3(kColThreads), 0, s, A);
+    }
+}
+
+}  // namespace
+}  // namespace snack
+
+using namespace snack;
+
+extern "C" snack_status snack_rmsnorm_fwd(const float* X, const void* R, int32_t h_fmt, const float* gain, float eps,
+                                          int64_t rows, int64_t n, void* H, float* Y, float* rstd, int32_t q_fmt,
+                                          uint8_t* Q, uint8_t* S, snack_stream stream)
+{
+    if (rows < 0 || n < 1 || !(eps >= 0.0f) || (h_fmt != SNACK_F32 && h_fmt != SNACK_BF16)) return SNACK_ERR_INVALID_ARG;
+    if (bad_size(rows, n)) return SNACK_ERR_UNSUPPORTED;
+    if (rows == 0) return SNACK_OK;
+    if (!X || !gain || !rstd || !R != !H || !Q != !S || (Q && !ckpt_format(q_fmt)) || (!Y && !Q))
+        return SNACK_ERR_INVALID_ARG;
+    const uintptr_t ha = h_fmt == SNACK_BF16 ? 2 : 4;
+    if (misaligned(X, 4) || misaligned(gain, 4) || misaligned(rstd, 4) || misaligned(Y, 4) || misaligned(R, ha) ||
+        misaligned(H, ha) || misaligned(Q, 16))
+        return SNACK_ERR_INVALID_ARG;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    ProfScope prof(KC_NORM, s);
+    const FwdArgs A{X, R, gain, H, Y, rstd, Q, S, rows, n, (n + kCkptBlock - 1) / kCkptBlock, eps};
+    const int qf = Q ? q_fmt : (int)SNACK_F32;
+    if (h_fmt == SNACK_BF16 && R) launch_fwd<SNACK_BF16>(A, qf, s);
+    else launch_fwd<SNACK_F32>(A, qf, s);
+    SNACK_HIP(hipGetLastError());
+    return SNACK_OK;
+}
+
+extern "C" snack_status snack_rmsnorm_bwd_work(int64_t rows, int64_t n, int64_t* bytes)
+{
+    if (!bytes || rows < 0 || n < 1) return SNACK_ERR_INVALID_ARG;
+    if (bad_size(rows, n)) return SNACK_ERR_UNSUPPORTED;
+    *bytes = 4 * ((int64_t)bwd_groups(rows, n) * n + (n > kRowMax ? rows : 0));
+    return SNACK_OK;
+}
+
+extern "C" snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int32_t h_fmt, const float* gain,
+                                          const float* rstd, const float* dY, const float* dR, int64_t rows, int64_t n,
+                                          float* dX, float* dgain, void* work, int64_t work_bytes, snack_stream stream)
+{
+    if (rows < 0 || n < 1) return SNACK_ERR_INVALID_ARG;
+    if (h_fmt != SNACK_F32 && h_fmt != SNACK_BF16 && !ckpt_format(h_fmt)) return SNACK_ERR_INVALID_ARG;
+    if (bad_size(rows, n)) return SNACK_ERR_UNSUPPORTED;
+    int64_t need = 0;
+    SNACK_CHECK(snack_rmsnorm_bwd_work(rows, n, &need));
+    if (rows > 0) {
+        if (!H || (ckpt_format(h_fmt) && !HS) || !gain || !rstd || !dY || !dX) return SNACK_ERR_INVALID_ARG;
+        const uintptr_t ha = ckpt_format(h_fmt) ? 16 : h_fmt == SNACK_BF16 ? 2 : 4;
+        if (misaligned(H, ha) || misaligned(gain, 4) || misaligned(rstd, 4) || misaligned(dY, 4) ||
+            misaligned(dR, 4) || misaligned(dX, 4))
+            return SNACK_ERR_INVALID_ARG;
+        if (dgain || n > kRowMax) {
+            if (!work || misaligned(work, 4)) return SNACK_ERR_INVALID_ARG;
+            if (work_bytes < need) return SNACK_ERR_WORKSPACE;
+        }
+    }
+    if (misaligned(dgain, 4)) return SNACK_ERR_INVALID_ARG;
+    if (rows == 0 && !dgain) return SNACK_OK;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    ProfScope prof(KC_NORM, s);
+    const int groups = bwd_groups(rows, n);
+    float* mean = (float*)work;
+    float* part = (float*)work + (n > kRowMax ? rows : 0);
+    if (rows > 0) {
+        const BwdArgs A{H, HS, gain, rstd, dY, dR, dX, dgain ? part : nullptr, mean, rows, n,
+                        (n + kCkptBlock - 1) / kCkptBlock};
+        switch (h_fmt) {
+        case SNACK_F32: launch_bwd<SNACK_F32>(A, groups, s); break;
+        case SNACK_BF16: launch_bwd<SNACK_BF16>(A, groups, s); break;
+        case SNACK_INT8: launch_bwd<SNACK_INT8>(A, groups, s); break;
+        default: launch_bwd<SNACK_E4M3>(A, groups, s); break;
+        }
+        SNACK_HIP(hipGetLastError());
+    }
+    if (dgain) {
+        // no rows: no partial rows, and the sum over none of them is 0
+        hipLaunchKernelGGL(part_sum_kernel, dim3((unsigned)((n + kSumCols - 1) / kSumCols)),
+                           dim3(kSumCols * kSumRows), 0, s, part, groups, n, dgain);
+        SNACK_HIP(hipGetLastError());
+    }
+    return SNACK_OK;
+}

@@ -26,7 +26,8 @@ int64_t g_tag = 0;
 std::map<std::pair<int, int64_t>, std::pair<int64_t, double>> g_tagged;
 
 const char* const g_names[KC_COUNT] = {"spmm_forward", "spmm_dx", "sddmm_dw", "transpose", "vals_t_refresh",
-                                       "sgd", "elementwise", "radix_sort", "canonicalise", "prune_regrow"};
+                                       "sgd", "elementwise", "radix_sort", "canonicalise", "prune_regrow",
+                                       "checkpoint", "rmsnorm"};
 
 hipEvent_t get_event()
 {

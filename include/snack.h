@@ -323,6 +323,98 @@ snack_status snack_gelu_fwd(const float* X, float* Y, int64_t n, snack_stream st
 snack_status snack_gelu_bwd(const float* X, const float* dY, float* dX, int64_t n, snack_stream stream);
 
 /*
+ * Activation checkpoints in 8 bits, and the operators of a transformer block
+ * that make and read them: with the weights sparse, the activations kept for
+ * the backward pass are what fills a training step's memory, and these take
+ * 33/32 of a byte a value.  Rows are tokens, n the features of one, arrays
+ * contiguous as everywhere here.
+ *
+ * A checkpoint of X [rows, n] is two device arrays: codes Q [rows, 32 ceil(n / 32)],
+ * one byte a value (16-byte aligned), and exponent bytes S [rows, ceil(n / 32)],
+ * one for every block of 32 consecutive features of a row.  A code c in a block
+ * with exponent byte s stands for c * 2^(s - 127); c is a signed integer of at
+ * most 127 in magnitude (SNACK_INT8) or an e4m3 number of at most 448
+ * (SNACK_E4M3).  s is the smallest value >= 1 for which the block's largest |x|
+ * stays in that range (a block of zeros has 1), and every value is rounded once,
+ * nearest even.  A block that holds a NaN or an infinity gets s = 255 and codes
+ * 0, and reads back as NaN throughout; a value that rounds up to 2^128 reads back as
+ * an infinity.  Codes past the n-th are 0 when written
+ * and never read as values.
+ *
+ * These calls allocate nothing, never synchronise, use no atomics (repeated
+ * calls give the same bits), and may be captured in a HIP graph.  rows = 0 is
+ * allowed and does nothing (dgain is then 0).  rows and n below 2^31 and blocks
+ * below 2^31, else SNACK_ERR_UNSUPPORTED.  No output may overlap an input.
+ */
+#define SNACK_F32 0    /* 32-bit floats */
+#define SNACK_BF16 1   /* bfloat16 */
+#define SNACK_INT8 2   /* checkpoint of signed integers */
+#define SNACK_E4M3 3   /* checkpoint of e4m3 numbers */
+
+/* Q, S = the checkpoint (fmt SNACK_INT8 or SNACK_E4M3) of X, device float[rows, n]. */
+snack_status snack_ckpt_pack(const float* X, int64_t rows, int64_t n, int32_t fmt, uint8_t* Q, uint8_t* S,
+                             snack_stream stream);
+/* Y [rows, n] = the values of a checkpoint, as SNACK_F32 (exact) or SNACK_BF16
+ * (exact down to steps of 2^-133, where bfloat16's end; nearest even below). */
+snack_status snack_ckpt_unpack(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t n, int32_t fmt, void* Y,
+                               int32_t y_fmt, snack_stream stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = X + R,   y = h rstd gain,   rstd = 1 / sqrt(mean over the row of h^2 + eps).
+ * The sum of squares is held in fp32.
+ *   X     device float[rows, n];  gain device float[n];  eps >= 0.
+ *   R, H  the residual stream before and after, device [rows, n] in h_fmt
+ *         (SNACK_F32, or SNACK_BF16: the sum is rounded to it once and the norm
+ *         is taken of the rounded h).  Both NULL: h is X.
+ *   Y     device float[rows, n], or NULL where only the checkpoint is wanted.
+ *   rstd  device float[rows], written (the backward takes it).
+ *   Q, S  the checkpoint of y in q_fmt, or both NULL (q_fmt is then ignored).
+ */
+snack_status snack_rmsnorm_fwd(const float* X, const void* R, int32_t h_fmt, const float* gain, float eps,
+                               int64_t rows, int64_t n, void* H, float* Y, float* rstd, int32_t q_fmt, uint8_t* Q,
+                               uint8_t* S, snack_stream stream);
+/*
+ * Its gradient.  With xh = h rstd and w = dY gain:
+ *   dX    = rstd (w - xh mean(w xh)) + dR       (the gradient of both X and R)
+ *   dgain = sum over rows of dY xh
+ *   H, HS    h as SNACK_F32 or SNACK_BF16 [rows, n] (HS NULL), or as a checkpoint
+ *            (codes, exponent bytes) in SNACK_INT8 or SNACK_E4M3.
+ *   rstd     the forward's, of the h before it was kept.
+ *   dR       device float[rows, n]: the gradient that reaches h along the
+ *            residual stream, or NULL for none.
+ *   dX       device float[rows, n];  dgain device float[n], or NULL.
+ *   work     device scratch of snack_rmsnorm_bwd_work bytes, used within the
+ *            call (SNACK_ERR_WORKSPACE when work_bytes is less); may be NULL
+ *            where dgain is NULL and n <= 16384.
+ */
+snack_status snack_rmsnorm_bwd_work(int64_t rows, int64_t n, int64_t* bytes);
+snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int32_t h_fmt, const float* gain, const float* rstd,
+                               const float* dY, const float* dR, int64_t rows, int64_t n, float* dX, float* dgain,
+                               void* work, int64_t work_bytes, snack_stream stream);
+
+/*
+ * Exact GELU, y = x Phi(x), that leaves the checkpoints of its input (for its
+ * own gradient) and of its output (for the next layer's), and that gradient,
+ * dX = dY (Phi(x) + x phi(x)) with x read from the checkpoint.  Y, the pair
+ * QX, SX and the pair QY, SY may each be NULL, not all three.  (Phi is computed
+ * from its own approximation, within 2e-7: not bit for bit snack_gelu_fwd.)
+ */
+snack_status snack_gelu_ckpt_fwd(const float* X, int64_t rows, int64_t n, int32_t fmt, float* Y, uint8_t* QX,
+                                 uint8_t* SX, uint8_t* QY, uint8_t* SY, snack_stream stream);
+snack_status snack_gelu_ckpt_bwd(const uint8_t* QX, const uint8_t* SX, const float* dY, int64_t rows, int64_t n,
+                                 int32_t fmt, float* dX, snack_stream stream);
+
+/*
+ * snack_backward with the forward's input read from its checkpoint Q, S of
+ * [B, K] in fmt: dX = dY W, and dW[k] = sum_b dY[b, r_k] x[b, c_k] with x the
+ * values the checkpoint stands for.  dX, dW, B, the workspace and the refusals
+ * as there.
+ */
+snack_status snack_backward_ckpt(snack_layer* layer, const uint8_t* Q, const uint8_t* S, int32_t fmt, const float* dY,
+                                 float* dX, float* dW, int32_t B, snack_stream stream);
+
+/*
  * Kernel timing.  While enabled, the library brackets each of its kernel
  * launches with HIP events recorded on the launch stream; snack_profile_read
  * synchronises those events and returns, for one kernel class, the launch count
