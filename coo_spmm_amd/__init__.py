@@ -11,7 +11,6 @@ PyTorch is used only for device memory and streams.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -399,41 +398,46 @@ def profile_snapshot():
 # Activation checkpoints, the norm and the GELU (tensors made by the call)
 # ---------------------------------------------------------------------------
 
+# These calls are a few microseconds of GPU work at the smallest sizes, so the host side is kept short: one check of
+# each tensor, one allocation for a checkpoint, and no stream object.  With `stream`, the call and the tensors it
+# makes are that stream's.
+
 _HIDDEN = {torch.float32: F32, torch.bfloat16: BF16}
 _BLOCK = 32   # features of a row that share one exponent byte
+_FLOAT, _BYTE = torch.float32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(stream):
-    """Tensors made inside belong to the stream the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _like(t, shape, name, ref, dtype=torch.float32):
-    """t is a contiguous tensor of this dtype and shape on ref's device."""
+def _arg(t, shape, name, dev, dtype=_FLOAT):
+    """The address of t, a contiguous tensor of this dtype and shape on GPU `dev`."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != ref.device:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the same GPU as the other tensors")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _matrix(t, name, dtype=torch.float32):
+def _rows(t, name, dtype=_FLOAT):
+    """rows, features, address and GPU of t, a contiguous [rows, features] tensor on the current GPU."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dim() != 2 or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [rows, features], got {tuple(t.shape)}")
-    _like(t, t.shape, name, t, dtype)
-    return t.shape
-
-
-def _kept_format(fmt):
-    if fmt not in (INT8, E4M3):
-        raise ValueError("a checkpoint's format is INT8 or E4M3")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be [rows, features], got {tuple(shape)}")
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return shape[0], shape[1], t.data_ptr(), dev
 
 
 class Ckpt:
@@ -441,55 +445,83 @@ class Ckpt:
     32 features of a row, s [rows, ceil(n / 32)] (uint8 device tensors); a code c stands for c * 2^(s - 127), c a
     signed integer (INT8) or an e4m3 number (E4M3).  33/32 bytes a value."""
 
-    __slots__ = ("q", "s", "fmt", "n")
+    __slots__ = ("rows", "n", "fmt", "_q", "_s", "_buf")
 
     def __init__(self, q, s, fmt, n):
-        _kept_format(fmt)
-        n = int(n)
+        if fmt != INT8 and fmt != E4M3:
+            raise ValueError("a checkpoint's format is INT8 or E4M3")
         if n < 1:
             raise ValueError("a checkpoint has at least one feature")
         nb = -(-n // _BLOCK)
-        rows = _matrix(q, "q", torch.uint8)[0]
-        _like(q, (rows, _BLOCK * nb), "q", q, torch.uint8)
-        _like(s, (rows, nb), "s", q, torch.uint8)
-        self.q, self.s, self.fmt, self.n = q, s, fmt, n
+        rows, width, _, dev = _rows(q, "q", _BYTE)
+        if width != _BLOCK * nb:
+            raise ValueError(f"q must have {_BLOCK * nb} bytes a row, got {width}")
+        _arg(s, (rows, nb), "s", dev, _BYTE)
+        self.rows, self.n, self.fmt, self._q, self._s, self._buf = rows, n, fmt, q, s, None
 
     @classmethod
-    def empty(cls, rows, n, fmt, device):
-        """Room for a checkpoint, on the current stream."""
-        _kept_format(fmt)
-        nb = -(-n // _BLOCK)
+    def _room(cls, like, rows, n, fmt):
+        """Room for a checkpoint beside `like`: codes and exponent bytes in one allocation."""
+        if fmt != INT8 and fmt != E4M3:
+            raise ValueError("a checkpoint's format is INT8 or E4M3")
         ck = cls.__new__(cls)
-        ck.q = torch.empty((rows, _BLOCK * nb), dtype=torch.uint8, device=device)
-        ck.s = torch.empty((rows, nb), dtype=torch.uint8, device=device)
-        ck.fmt, ck.n = fmt, n
+        ck.rows, ck.n, ck.fmt, ck._q, ck._s = rows, n, fmt, None, None
+        ck._buf = like.new_empty(rows * -(-n // _BLOCK) * (_BLOCK + 1), dtype=_BYTE)
         return ck
+
+    def _ptrs(self):
+        if self._buf is None:
+            return self._q.data_ptr(), self._s.data_ptr()
+        p = self._buf.data_ptr()
+        return p, p + self.rows * -(-self.n // _BLOCK) * _BLOCK
+
+    def _dev(self):
+        return (self._q if self._buf is None else self._buf).get_device()
+
+    @property
+    def q(self):
+        if self._q is None:
+            nb = -(-self.n // _BLOCK)
+            self._q = self._buf[: self.rows * nb * _BLOCK].view(self.rows, nb * _BLOCK)
+        return self._q
+
+    @property
+    def s(self):
+        if self._s is None:
+            nb = -(-self.n // _BLOCK)
+            self._s = self._buf[self.rows * nb * _BLOCK:].view(self.rows, nb)
+        return self._s
+
+    @property
+    def nbytes(self):
+        return self.rows * -(-self.n // _BLOCK) * (_BLOCK + 1)
 
     @classmethod
     def pack(cls, x, fmt, stream=None):
         """The checkpoint of x, float32 [rows, n]."""
-        rows, n = _matrix(x, "x")
-        with _on(stream):
-            ck = cls.empty(rows, n, fmt, x.device)
-        snack_ckpt_pack(x, fmt, ck.q, ck.s, stream)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return cls.pack(x, fmt)
+        rows, n, px, dev = _rows(x, "x")
+        ck = cls._room(x, rows, n, fmt)
+        q, s = ck._ptrs()
+        _check(_lib.snack_ckpt_pack(px, rows, n, fmt, q, s, _raw_stream(dev)), "snack_ckpt_pack")
         return ck
 
     def unpack(self, dtype=torch.float32, stream=None):
         """The values it stands for, in float32 or bfloat16."""
-        if dtype not in _HIDDEN:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.unpack(dtype)
+        y_fmt = _HIDDEN.get(dtype)
+        if y_fmt is None:
             raise TypeError("a checkpoint is read as float32 or bfloat16")
-        with _on(stream):
-            y = torch.empty((self.rows, self.n), dtype=dtype, device=self.q.device)
-        snack_ckpt_unpack(self.q, self.s, self.fmt, y, _HIDDEN[dtype], stream)
+        own = self._q if self._buf is None else self._buf
+        y = own.new_empty((self.rows, self.n), dtype=dtype)
+        q, s = self._ptrs()
+        _check(_lib.snack_ckpt_unpack(q, s, self.rows, self.n, self.fmt, y.data_ptr(), y_fmt,
+                                      _raw_stream(own.get_device())), "snack_ckpt_unpack")
         return y
-
-    @property
-    def rows(self):
-        return self.q.shape[0]
-
-    @property
-    def nbytes(self):
-        return self.q.numel() + self.s.numel()
 
 
 def rmsnorm_fwd(x, gain, eps, residual=None, q_format=None, want_y=True, stream=None):
@@ -497,73 +529,91 @@ def rmsnorm_fwd(x, gain, eps, residual=None, q_format=None, want_y=True, stream=
 
     residual: float32 or bfloat16 [rows, n]; h has its type (None: h is x itself).  q_format: INT8 or E4M3 also
     leaves y's checkpoint; with want_y=False only that.  Returns (h, y, rstd, checkpoint), None where there is none."""
-    rows, n = _matrix(x, "x")
-    _like(gain, (n,), "gain", x)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm_fwd(x, gain, eps, residual, q_format, want_y)
+    rows, n, px, dev = _rows(x, "x")
+    pg = _arg(gain, (n,), "gain", dev)
     if not want_y and q_format is None:
         raise ValueError("neither y nor its checkpoint is wanted")
-    h_fmt, h, y, ck = F32, None, None, None
+    h_fmt, h, pr, ph = F32, x, None, None
     if residual is not None:
-        if not isinstance(residual, torch.Tensor) or residual.dtype not in _HIDDEN:
+        h_fmt = _HIDDEN.get(getattr(residual, "dtype", None))
+        if h_fmt is None:
             raise TypeError("residual must be a float32 or bfloat16 tensor")
-        _like(residual, x.shape, "residual", x, residual.dtype)
-        h_fmt = _HIDDEN[residual.dtype]
-    with _on(stream):
-        if residual is not None:
-            h = torch.empty_like(residual)
-        if want_y:
-            y = torch.empty_like(x)
-        rstd = x.new_empty((rows,))
-        if q_format is not None:
-            ck = Ckpt.empty(rows, n, q_format, x.device)
-    snack_rmsnorm_fwd(x, residual, h_fmt, gain, eps, h, y, rstd, F32 if ck is None else ck.fmt,
-                      None if ck is None else ck.q, None if ck is None else ck.s, stream)
-    return (x if h is None else h), y, rstd, ck
+        pr = _arg(residual, x.shape, "residual", dev, residual.dtype)
+        h = torch.empty_like(residual)
+        ph = h.data_ptr()
+    y = torch.empty_like(x) if want_y else None
+    rstd = x.new_empty(rows)
+    ck, q, s = None, None, None
+    if q_format is not None:
+        ck = Ckpt._room(x, rows, n, q_format)
+        q, s = ck._ptrs()
+    _check(_lib.snack_rmsnorm_fwd(px, pr, h_fmt, pg, eps, rows, n, ph, y.data_ptr() if want_y else None,
+                                  rstd.data_ptr(), F32 if ck is None else q_format, q, s, _raw_stream(dev)),
+           "snack_rmsnorm_fwd")
+    return h, y, rstd, ck
 
 
 def rmsnorm_bwd(h, gain, rstd, dY, dR=None, want_dgain=True, stream=None):
     """The gradient of rmsnorm_fwd: h as float32 or bfloat16 [rows, n] or as a Ckpt, rstd the forward's, dY float32,
     dR the gradient that reaches h along the residual stream (None: none).  Returns (dX, dgain): dX is the gradient
     of both x and residual, dgain None where it is not wanted."""
-    rows, n = _matrix(dY, "dY")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rmsnorm_bwd(h, gain, rstd, dY, dR, want_dgain)
+    rows, n, pd, dev = _rows(dY, "dY")
     if isinstance(h, Ckpt):
-        if (h.rows, h.n) != (rows, n):
+        if h.rows != rows or h.n != n:
             raise ValueError(f"h must have shape {(rows, n)}, got {(h.rows, h.n)}")
-        if h.q.device != dY.device:
+        if h._dev() != dev:
             raise ValueError("h must be on the same GPU as the other tensors")
-        H, HS, fmt = h.q, h.s, h.fmt
+        fmt = h.fmt
+        ph, ps = h._ptrs()
     else:
-        if not isinstance(h, torch.Tensor) or h.dtype not in _HIDDEN:
+        fmt = _HIDDEN.get(getattr(h, "dtype", None))
+        if fmt is None:
             raise TypeError("h must be a float32 or bfloat16 tensor or a Ckpt")
-        _like(h, dY.shape, "h", dY, h.dtype)
-        H, HS, fmt = h, None, _HIDDEN[h.dtype]
-    _like(gain, (n,), "gain", dY)
-    _like(rstd, (rows,), "rstd", dY)
-    if dR is not None:
-        _like(dR, dY.shape, "dR", dY)
-    with _on(stream):
-        dX = torch.empty_like(dY)
-        dgain = dY.new_empty((n,)) if want_dgain else None
-        work = torch.empty(snack_rmsnorm_bwd_work(rows, n), dtype=torch.uint8, device=dY.device)
-    snack_rmsnorm_bwd(H, HS, fmt, gain, rstd, dY, dR, dX, dgain, work, stream)
+        ph, ps = _arg(h, dY.shape, "h", dev, h.dtype), None
+    pg, pt = _arg(gain, (n,), "gain", dev), _arg(rstd, (rows,), "rstd", dev)
+    pr = None if dR is None else _arg(dR, dY.shape, "dR", dev)
+    dX = torch.empty_like(dY)
+    dgain = torch.empty_like(gain) if want_dgain else None
+    nbytes = snack_rmsnorm_bwd_work(rows, n)
+    work = dY.new_empty(nbytes, dtype=_BYTE)
+    _check(_lib.snack_rmsnorm_bwd(ph, ps, fmt, pg, pt, pd, pr, rows, n, dX.data_ptr(),
+                                  dgain.data_ptr() if want_dgain else None, work.data_ptr(), nbytes,
+                                  _raw_stream(dev)), "snack_rmsnorm_bwd")
     return dX, dgain
 
 
 def gelu_ckpt_fwd(x, fmt, want_y=True, stream=None):
     """Exact GELU of x, float32 [rows, n].  Returns (y, checkpoint of x, checkpoint of y)."""
-    rows, n = _matrix(x, "x")
-    with _on(stream):
-        y = torch.empty_like(x) if want_y else None
-        cx, cy = Ckpt.empty(rows, n, fmt, x.device), Ckpt.empty(rows, n, fmt, x.device)
-    snack_gelu_ckpt_fwd(x, fmt, y, cx.q, cx.s, cy.q, cy.s, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gelu_ckpt_fwd(x, fmt, want_y)
+    rows, n, px, dev = _rows(x, "x")
+    y = torch.empty_like(x) if want_y else None
+    cx, cy = Ckpt._room(x, rows, n, fmt), Ckpt._room(x, rows, n, fmt)
+    qx, sx = cx._ptrs()
+    qy, sy = cy._ptrs()
+    _check(_lib.snack_gelu_ckpt_fwd(px, rows, n, fmt, y.data_ptr() if want_y else None, qx, sx, qy, sy,
+                                    _raw_stream(dev)), "snack_gelu_ckpt_fwd")
     return y, cx, cy
 
 
 def gelu_ckpt_bwd(ck, dY, stream=None):
     """dY (Phi(x) + x phi(x)) with x read from its checkpoint; dY float32 [rows, n]."""
-    _like(dY, (ck.rows, ck.n), "dY", ck.q)
-    with _on(stream):
-        dX = torch.empty_like(dY)
-    snack_gelu_ckpt_bwd(ck.q, ck.s, ck.fmt, dY, dX, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gelu_ckpt_bwd(ck, dY)
+    dev = ck._dev()
+    pd = _arg(dY, (ck.rows, ck.n), "dY", dev)
+    dX = torch.empty_like(dY)
+    q, s = ck._ptrs()
+    _check(_lib.snack_gelu_ckpt_bwd(q, s, pd, ck.rows, ck.n, ck.fmt, dX.data_ptr(), _raw_stream(dev)),
+           "snack_gelu_ckpt_bwd")
     return dX
 
 
@@ -611,21 +661,26 @@ class SnackLayer:
 
     def backward_ckpt(self, ck, dY, want_dx=True, want_dw=True, dX=None, dW=None, stream=None):
         """backward() with its input read from a checkpoint (Ckpt of [B, K]); returns (dX, dW)."""
-        _like(dY, (ck.rows, self.M), "dY", ck.q)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward_ckpt(ck, dY, want_dx, want_dw, dX, dW)
+        rows, dev = ck.rows, ck._dev()
         if ck.n != self.K:
             raise ValueError(f"the checkpoint must have {self.K} features, got {ck.n}")
-        with _on(stream):
-            if want_dx and dX is None:
-                dX = dY.new_empty((ck.rows, self.K))
-            if want_dw and dW is None:
-                dW = dY.new_empty((self.nnz,))
-        dX, dW = (dX if want_dx else None), (dW if want_dw else None)
-        if dX is not None:
-            _like(dX, (ck.rows, self.K), "dX", ck.q)
-        if dW is not None:
-            _like(dW, (self.nnz,), "dW", ck.q)
-        snack_backward_ckpt(self.h, ck.q, ck.s, ck.fmt, dY, dX, dW if self.nnz else None, stream)
-        return dX, dW
+        pd = _arg(dY, (rows, self.M), "dY", dev)
+        px = pw = None
+        if want_dx:
+            if dX is None:
+                dX = dY.new_empty((rows, self.K))
+            px = _arg(dX, (rows, self.K), "dX", dev)
+        if want_dw:
+            if dW is None:
+                dW = dY.new_empty(self.nnz)
+            pw = _arg(dW, (self.nnz,), "dW", dev) or None
+        q, s = ck._ptrs()
+        _check(_lib.snack_backward_ckpt(self.h, q, s, ck.fmt, pd, px, pw, rows, _raw_stream(dev)),
+               "snack_backward_ckpt")
+        return (dX if want_dx else None), (dW if want_dw else None)
 
     def backward_sgd(self, X, dY, lr, want_dx=True, dX=None, dW=None, stream=None):
         import torch
