@@ -126,6 +126,13 @@ struct snack_layer {
     const float* dwt_for = nullptr;
     bool dwt_valid = false;
 
+    // the positions in tile order and the tiles' places in it, for the dW of
+    // dense enough layers by matrix instructions (sample.hip; else null),
+    // remade when the index changes
+    uint32_t* sample_list = nullptr;   // [cap]
+    int32_t* sample_ptr = nullptr;
+    mutable bool sample_valid = false;
+
     snack::View fwd;   // idx = cols
     snack::View tr;    // idx = rows_t
 
@@ -244,6 +251,16 @@ snack_status transpose_pad(const float* src, float* dst, int n, const float* src
 // The same copy from a checkpoint (codes Q, exponent bytes S) of src [B, n] (ckpt.hip)
 snack_status ckpt_transpose(const uint8_t* Q, const uint8_t* S, int fmt, int n, int B, int bp, float* xt,
                             hipStream_t s);
+
+// dW from a checkpoint by matrix instructions (sample.hip): whether a layer of
+// this size has the tile list, and whether a batch plan takes the path; the bytes
+// of the tiles' places and of the workspace; dW from Q, S and dY [B][M]
+bool sample_layer(int64_t M, int64_t K, int64_t nnz);
+bool sample_applies(const snack_layer* L, const BatchPlan& p);
+size_t sample_ptr_bytes(const snack_layer* L);
+size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p);
+snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
+                       float* dW, void* ws, hipStream_t s);
 
 // Whether every kernel of a forward (fwd) or backward (dx, dw requested) pass
 // can take the caller's batch-major [B][n] arrays directly, so no

@@ -55,7 +55,9 @@ size_t ws_need(const snack_layer* L, const BatchPlan& p)
 {
     const size_t a = (((size_t)L->K * p.bp * 4) + 255) & ~(size_t)255;
     const size_t b = (((size_t)L->M * p.bp * 4) + 255) & ~(size_t)255;
-    return a + b + tile_part_bytes(L, p) + wide_dw_bytes(L, p);
+    // the operands of the dW from a checkpoint are used up before a pass writes anything else here
+    const size_t rest = a + b + tile_part_bytes(L, p) + wide_dw_bytes(L, p), sample = sample_ws_bytes(L, p);
+    return rest > sample ? rest : sample;
 }
 
 // grow the workspace to hold plan p (never shrinks); the new buffer is
@@ -277,6 +279,10 @@ extern "C" snack_status snack_layer_create(int32_t M, int32_t K, int64_t nnz, co
         if (_s != SNACK_OK) return fail(_s);
         L->scratch_bytes = scr;
     }
+    if (sample_layer(M, K, nnz)) {
+        ALLOC(sample_list, uint32_t*, nb4);
+        ALLOC(sample_ptr, int32_t*, sample_ptr_bytes(L));
+    }
     // coherent pinned words the drop/regrow's kernels write its result into (system-scope stores)
     if (hipHostMalloc((void**)&L->host_res, 64, hipHostMallocMapped | hipHostMallocCoherent) != hipSuccess) {
         L->host_res = nullptr;
@@ -420,6 +426,11 @@ extern "C" snack_status snack_backward_ckpt(snack_layer* L, const uint8_t* Q, co
     if (!dW) return backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr);
     const BatchPlan p = plan_batch(B);
     SNACK_CHECK(ws_check(L, p));
+    if (sample_applies(L, p)) {
+        L->dwt_valid = false;
+        SNACK_CHECK(sample_dw(L, Q, S, fmt, dY, B, dW, L->ws, s));
+        return dX ? backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr) : SNACK_OK;
+    }
     // X as the passes of this plan read it, in the workspace's place for its feature-major copy
     if (p.bp == 1 || spmm_batch_major(L, p, false, dX != nullptr, true)) {
         SNACK_CHECK(snack_ckpt_unpack(Q, S, B, L->K, fmt, ws_x(L), SNACK_F32, stream));

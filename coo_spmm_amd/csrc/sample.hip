@@ -1,0 +1,422 @@
+// sample.hip -- dW on the support from a checkpointed input, by matrix instructions.
+//
+//   dW[k] = sum_b dY[b, r_k] x[b, c_k]
+//
+// Walking the stored positions costs every entry two operand rows of B values, so
+// past about one position in a hundred it is cheaper to compute whole tiles of
+// dY^T X on the matrix cores and keep only the stored positions.  A wavefront's
+// registers hold up to 64 x 128 cells; they go to LDS 32 rows at a time, from
+// where the stored ones are read and written to dW.  The dense product itself
+// never leaves the CU.
+//
+// Which cells are stored comes from a list in tile order (32 rows x 128 columns a
+// tile, row-major within it), made once after every change of the index: 4 bytes
+// a position, read in whole lines and known before the product starts.  (Reading
+// each row's run of column indices instead, eight lanes a row, left a dependent
+// load behind every run longer than eight: 65 us against NEWTIME at 10000 x 10000,
+// 95 %, 64 batch rows.)
+//
+// fp32 accuracy from bf16 instructions: an fp32 number is the exact sum of three
+// bf16 numbers (its 24 significant bits in three runs of eight, taken by
+// truncation, so nothing overflows), and a checkpoint's value has at most eight
+// significant bits, so it is one bf16 number.  Three products, each exact, are
+// added in fp32: what is rounded is the sums alone, as in a chain of fp32
+// multiply-adds.  Against a checkpoint this costs half of what two fp32
+// operands would (six products).
+//
+// split_operands_kernel writes both operands in the order in which the matrix
+// instruction takes them (32 rows or columns x 16 batch rows, a kilobyte, 16
+// bytes a lane), once, so the product's loads are whole kilobytes from L2 into
+// registers, without LDS and without barriers.
+#include "ckpt.h"
+#include <stdlib.h>
+
+namespace snack {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kStep = 16;             // batch rows of one instruction
+constexpr int kCols = 128;            // columns of a tile
+constexpr int kCB = kCols / 32;
+constexpr int kCellBits = 12;         // a cell of a tile: 32 x 128
+constexpr int kSampleMaxK = 32768;    // columns at most: a slot of a 32-row panel then fits the other 20 bits
+constexpr int kAhead = 4;             // list words a lane holds
+constexpr int kStage = 16 * kCols;    // cells a wavefront stages at once: half a tile
+constexpr int kXcd = 8;
+constexpr int kFragBytes = kWave * 16;   // one instruction's operand
+
+// the three bf16 parts of x (hi + mid + lo = x); an infinity or NaN is all in the first
+__device__ inline void split3(float x, uint16_t& hi, uint16_t& mid, uint16_t& lo)
+{
+    const uint32_t b = __float_as_uint(x);
+    const bool fin = (b & 0x7F800000u) != 0x7F800000u;
+    const float r1 = x - __uint_as_float(b & 0xFFFF0000u);
+    const uint32_t b1 = fin ? __float_as_uint(r1) : 0u;
+    const float r2 = __uint_as_float(b1) - __uint_as_float(b1 & 0xFFFF0000u);
+    const uint32_t nan = (b & 0x7FFFFFFFu) > 0x7F800000u ? 0x40u : 0u;
+    hi = (uint16_t)((b >> 16) | nan);
+    mid = (uint16_t)(b1 >> 16);
+    lo = (uint16_t)(__float_as_uint(r2) >> 16);
+}
+
+struct SplitArgs {
+    const float* dY;      // [B][M]
+    const uint8_t* Q;     // [B][32 per_row]
+    const uint8_t* S;     // [B][per_row]
+    uint4* A;             // [row blocks][steps][3][64]
+    uint4* X;             // [column blocks][steps][64]
+    int M, K, B, per_row, steps, rblocks, cblocks;
+};
+
+// A wavefront makes one block: lane l holds row (column) l % 32 and the eight
+// batch rows 8 (l / 32) ... of a step; rows, columns and batch rows past the
+// end are zeros.
+template <int FMT>
+__global__ void __launch_bounds__(256) split_operands_kernel(SplitArgs P)
+{
+    const int lane = (int)threadIdx.x & (kWave - 1);
+    const int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+    const int64_t na = (int64_t)P.rblocks * P.steps, nx = (int64_t)P.cblocks * P.steps;
+    if (w >= na + nx) return;
+    const bool first = w < na;
+    const int64_t v = first ? w : w - na;
+    // neighbouring wavefronts take neighbouring rows (columns) of the same batch rows
+    const int nb = first ? P.rblocks : P.cblocks;
+    const int step = (int)(v / nb), blk = (int)(v - (int64_t)step * nb);
+    const int c = blk * 32 + (lane & 31);
+    const int b0 = step * kStep + 8 * (lane >> 5);
+    if (first) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = (c < P.M && b0 + j < P.B) ? P.dY[(int64_t)(b0 + j) * P.M + c] : 0.0f;
+        uint16_t part[3][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split3(x[j], part[0][j], part[1][j], part[2][j]);
+        uint4* out = P.A + (((int64_t)blk * P.steps + step) * 3) * kWave + lane;
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            out[q * kWave] = make_uint4(part[q][0] | part[q][1] << 16, part[q][2] | part[q][3] << 16,
+                                        part[q][4] | part[q][5] << 16, part[q][6] | part[q][7] << 16);
+    } else {
+        uint16_t x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[j] = 0;
+            if (c < P.K && b0 + j < P.B) {
+                const int64_t row = (int64_t)(b0 + j) * P.per_row + blk;
+                const f32x4 v4 = ckpt_codes4<FMT>(P.Q[row * kCkptBlock + (lane & 31)]);
+                x[j] = bf16_bits(v4.x * ckpt_scale(P.S[row]));
+            }
+        }
+        P.X[((int64_t)blk * P.steps + step) * kWave + lane] =
+            make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+    }
+}
+
+// The tile list of one panel of 32 rows by one workgroup.  A panel's positions are
+// one run of the canonical order; the list holds the same run in tile order:
+// list[i] = (slot - panel's first slot) << 12 | row in panel * 128 + column in tile, and
+// tile_ptr[panel * tiles + t] the place of tile t's first.  Every entry's place follows from
+// where its row enters its tile, so nothing is counted by atomics.
+__global__ void __launch_bounds__(256) sample_list_kernel(const int32_t* __restrict__ ptr,
+                                                          const int32_t* __restrict__ cols, int M, int tiles,
+                                                          uint32_t* __restrict__ list, int32_t* __restrict__ tile_ptr)
+{
+    extern __shared__ int32_t at[];   // [32][tiles + 1]: a row's first entry in tile t or later; then [32][tiles] places
+    const int lane = (int)threadIdx.x & (kWave - 1), wave = (int)threadIdx.x / kWave;
+    const int r0 = (int)blockIdx.x * 32, nr = min(32, M - r0);
+    const int w = tiles + 1;
+    int32_t* place = at + 32 * w;
+    const int32_t base = ptr[r0];
+    for (int r = wave; r < 32; r += 4) {
+        const int32_t lo = r < nr ? ptr[r0 + r] : ptr[M], hi = r < nr ? ptr[r0 + r + 1] : ptr[M];
+        for (int32_t e = lo + lane; e < hi; e += kWave) {
+            const int t = cols[e] / kCols, before = e > lo ? cols[e - 1] / kCols : -1;
+            for (int s = before + 1; s <= t; ++s) at[r * w + s] = e;
+        }
+        const int last = hi > lo ? cols[hi - 1] / kCols : -1;
+        for (int s = last + 1 + lane; s <= tiles; s += kWave) at[r * w + s] = hi;
+    }
+    __syncthreads();
+    // a tile's entries before each row, then (one wavefront) the tiles' places
+    for (int t = (int)threadIdx.x; t < tiles; t += 256) {
+        int32_t n = 0;
+        for (int r = 0; r < 32; ++r) {
+            place[r * tiles + t] = n;
+            n += at[r * w + t + 1] - at[r * w + t];
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {
+        int32_t carry = base;
+        for (int t0 = 0; t0 < tiles; t0 += kWave) {
+            const int t = t0 + lane;
+            const int32_t n = t < tiles ? place[31 * tiles + t] + at[31 * w + t + 1] - at[31 * w + t] : 0;
+            int32_t x = n;
+            for (int d = 1; d < kWave; d <<= 1) {
+                const int32_t y = __shfl_up(x, d, kWave);
+                if (lane >= d) x += y;
+            }
+            const int32_t first = carry + x - n;
+            if (t < tiles) {
+                tile_ptr[(int64_t)blockIdx.x * tiles + t] = first;
+                for (int r = 0; r < 32; ++r) place[r * tiles + t] += first;
+            }
+            carry += __shfl(x, kWave - 1, kWave);
+        }
+        if (lane == 0 && blockIdx.x == gridDim.x - 1) tile_ptr[(int64_t)gridDim.x * tiles] = carry;
+    }
+    __syncthreads();
+    for (int r = wave; r < nr; r += 4) {
+        for (int32_t e = ptr[r0 + r] + lane; e < ptr[r0 + r + 1]; e += kWave) {
+            const int c = cols[e], t = c / kCols;
+            list[place[r * tiles + t] + e - at[r * w + t]] =
+                (uint32_t)(e - base) << kCellBits | (uint32_t)(r * kCols + c % kCols);
+        }
+    }
+}
+
+struct SampleArgs {
+    const uint4* A;
+    const uint4* X;
+    const uint32_t* list;
+    const int32_t* tile_ptr;
+    const int32_t* row_ptr;
+    float* dW;
+    int steps, rblocks, cblocks;
+    int panels, tiles;     // tiles of a wavefront down and across
+    int per_xcd;           // workgroups an XCD takes
+    uint32_t a_bytes, x_bytes;
+};
+
+// RB: 32-row blocks of a wavefront's tile.  KS: wavefronts of the workgroup that
+// share a tile, each a KS-th of the batch rows; their sums are added, in wavefront
+// order, where the positions are read.
+template <int RB, int KS>
+__global__ void __launch_bounds__(256, RB == 1 ? 4 : 2) sample_kernel(SampleArgs P)
+{
+    __shared__ float stage[4][kStage];
+    const int lane = (int)threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const int ks = wave % KS;
+    // an XCD takes a contiguous run of tiles, column tiles first: a panel's rows stay in its L2, and
+    // the pieces of a row's dW that neighbouring tiles write meet there
+    const int64_t unit = (int64_t)(blockIdx.x % kXcd) * P.per_xcd + blockIdx.x / kXcd;
+    const int64_t tile = unit * (4 / KS) + wave / KS;
+    if (tile >= (int64_t)P.panels * P.tiles) return;   // with KS > 1 the whole workgroup
+    const int panel = (int)((uint32_t)tile / (uint32_t)P.tiles);
+    const int ct = (int)((uint32_t)tile - (uint32_t)panel * (uint32_t)P.tiles);
+
+    // the first positions this wavefront stores: the words ks * 64 + lane, + 64 KS, ... of each tile's list
+    int32_t p1[RB], pos[RB];
+    uint32_t word[RB][kAhead];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int rp = panel * RB + rb;
+        const bool ok = rp < P.rblocks;
+        const int64_t id = (int64_t)min(rp, P.rblocks - 1) * P.tiles + ct;
+        pos[rb] = P.tile_ptr[id] + ks * kWave + lane;
+        p1[rb] = ok ? P.tile_ptr[id + 1] : 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)   // the list is padded: reads past the tile's end stay in bounds
+            word[rb][k] = P.list[pos[rb] + k * KS * kWave];
+    }
+
+    f32x16 acc[RB][kCB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[rb][cb][i] = 0.0f;
+
+    if (ks < P.steps) {
+        // Loads through buffer descriptors: the block's offset is a scalar, the lane's a constant, and a
+        // load stays where it is written (an ordinary load that is carried round the loop gets moved to
+        // its use).  Blocks past the matrix repeat the last one (their cells hold no position).
+        const auto ra = __builtin_amdgcn_make_buffer_rsrc((void*)P.A, 0, P.a_bytes, 0x00027000);
+        const auto rx = __builtin_amdgcn_make_buffer_rsrc((void*)P.X, 0, P.x_bytes, 0x00027000);
+        const int at = lane * 16;
+        auto frag_a = [&](uint32_t blk) {
+            return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ra, at, (int)(blk * kFragBytes), 0));
+        };
+        auto frag_x = [&](uint32_t blk) {
+            return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rx, at, (int)(blk * kFragBytes), 0));
+        };
+        uint32_t a[RB], x[kCB];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) a[rb] = (uint32_t)min(panel * RB + rb, P.rblocks - 1) * P.steps * 3;
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb) x[cb] = (uint32_t)min(ct * kCB + cb, P.cblocks - 1) * P.steps;
+        // one set of A registers, each refilled for the next step as soon as its products are issued, and
+        // two of X: with the sums that is what fits at two wavefronts a SIMD
+        bf16x8 fa[RB][3], fx[kCB], nx[kCB];
+#pragma unroll
+        for (int cb = 0; cb < kCB; ++cb) fx[cb] = frag_x(x[cb] + ks);
+#pragma unroll
+        for (int q = 2; q >= 0; --q) {   // in the loop's order, so that its waits need not be wider
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) fa[rb][q] = frag_a(a[rb] + ks * 3 + q);
+        }
+#pragma unroll 1
+        for (int s = ks; s < P.steps; s += KS) {
+            const int next = min(s + KS, P.steps - 1);   // past the last step the loads repeat it
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb) nx[cb] = frag_x(x[cb] + next);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = 2; q >= 0; --q) {   // the smallest part first
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+                    for (int cb = 0; cb < kCB; ++cb)
+                        acc[rb][cb] =
+                            __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[rb][q], fx[cb], acc[rb][cb], 0, 0, 0);
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) fa[rb][q] = frag_a(a[rb] + next * 3 + q);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb) fx[cb] = nx[cb];
+        }
+    }
+
+    float* mine = stage[wave];
+    const float* group = stage[wave - ks];
+    // half a tile at a time goes through LDS, so that four workgroups fit on a CU
+    auto settle = [&] {
+        if constexpr (KS > 1) {
+            __syncthreads();
+        } else {
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+    };
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        float* out = P.dW + P.row_ptr[min(panel * RB + rb, P.rblocks - 1) * 32];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (rb + half > 0) settle();
+            // lane l holds column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4 of each 32 x 32 block
+#pragma unroll
+            for (int cb = 0; cb < kCB; ++cb)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    mine[(8 * (i / 4) + 4 * (lane >> 5) + (i & 3)) * kCols + cb * 32 + (lane & 31)] =
+                        acc[rb][cb][8 * half + i];
+            settle();
+            auto put = [&](uint32_t w, int32_t e) {
+                const int cell = (int)(w & ((1u << kCellBits) - 1)) - half * kStage;
+                if (e < p1[rb] && (uint32_t)cell < (uint32_t)kStage) {
+                    float v = group[cell];
+#pragma unroll
+                    for (int j = 1; j < KS; ++j) v += group[cell + j * kStage];
+                    out[w >> kCellBits] = v;
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) put(word[rb][k], pos[rb] + k * KS * kWave);
+            for (int32_t e = pos[rb] + kAhead * KS * kWave; e < p1[rb]; e += kAhead * KS * kWave) {
+                uint32_t more[kAhead];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) more[k] = P.list[e + k * KS * kWave];
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) put(more[k], e + k * KS * kWave);
+            }
+        }
+    }
+}
+
+inline int blocks32(int n) { return (n + 31) / 32; }
+
+}  // namespace
+
+// Where the tiles beat the walk over the positions: at least one position in 64 cells, and 16 batch rows
+// (an instruction's depth); operands below 4 GB (buffer offsets).
+bool sample_layer(int64_t M, int64_t K, int64_t nnz) { return nnz > 0 && K <= kSampleMaxK && nnz >= M * K / 64; }
+bool sample_applies(const snack_layer* L, const BatchPlan& p)
+{
+    const int64_t steps = (p.bp + kStep - 1) / kStep;
+    return L->sample_list && p.bp >= kStep && steps * 3 * blocks32(L->M) < (1ll << 32) / kFragBytes &&
+           steps * blocks32(L->K) < (1ll << 32) / kFragBytes;
+}
+
+size_t sample_ptr_bytes(const snack_layer* L)
+{
+    return ((size_t)((L->K + kCols - 1) / kCols) * blocks32(L->M) + 1) * sizeof(int32_t);
+}
+
+size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p)
+{
+    if (!sample_applies(L, p)) return 0;
+    const size_t steps = (size_t)(p.bp + kStep - 1) / kStep;
+    return steps * kWave * sizeof(uint4) * (3 * (size_t)blocks32(L->M) + blocks32(L->K));
+}
+
+snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
+                       float* dW, void* ws, hipStream_t s)
+{
+    ProfScope prof(KC_SDDMM_DW, s);
+    const int tiles = (L->K + kCols - 1) / kCols;
+    if (!L->sample_valid) {
+        hipLaunchKernelGGL(sample_list_kernel, dim3((unsigned)blocks32(L->M)), dim3(256),
+                           (size_t)32 * (2 * tiles + 1) * sizeof(int32_t), s, L->row_ptr, L->cols, L->M, tiles,
+                           L->sample_list, L->sample_ptr);
+        SNACK_HIP(hipGetLastError());
+        // a list recorded into a graph is only made when the graph runs: eager calls make their own
+        hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+        SNACK_HIP(hipStreamIsCapturing(s, &cap));
+        L->sample_valid = cap == hipStreamCaptureStatusNone;
+    }
+    SplitArgs a;
+    a.dY = dY;
+    a.Q = Q;
+    a.S = S;
+    a.M = L->M;
+    a.K = L->K;
+    a.B = B;
+    a.per_row = blocks32(L->K);
+    a.steps = (B + kStep - 1) / kStep;
+    a.rblocks = blocks32(L->M);
+    a.cblocks = blocks32(L->K);
+    a.A = (uint4*)ws;
+    a.X = a.A + (size_t)a.rblocks * a.steps * 3 * kWave;
+    const int64_t waves = (int64_t)(a.rblocks + a.cblocks) * a.steps;
+    const auto split = fmt == SNACK_INT8 ? split_operands_kernel<SNACK_INT8> : split_operands_kernel<SNACK_E4M3>;
+    hipLaunchKernelGGL(split, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a);
+    SNACK_HIP(hipGetLastError());
+
+    SampleArgs t;
+    t.A = a.A;
+    t.X = a.X;
+    t.list = L->sample_list;
+    t.tile_ptr = L->sample_ptr;
+    t.row_ptr = L->row_ptr;
+    t.dW = dW;
+    t.steps = a.steps;
+    t.rblocks = a.rblocks;
+    t.cblocks = a.cblocks;
+    t.a_bytes = (uint32_t)a.rblocks * a.steps * 3 * kFragBytes;
+    t.x_bytes = (uint32_t)a.cblocks * a.steps * kFragBytes;
+    t.tiles = tiles;
+    auto go = [&](auto kern, int rb, int ks) {
+        t.panels = (a.rblocks + rb - 1) / rb;
+        const int64_t units = ((int64_t)t.panels * tiles + 4 / ks - 1) / (4 / ks);
+        t.per_xcd = (int)((units + kXcd - 1) / kXcd);
+        hipLaunchKernelGGL(kern, dim3((unsigned)(t.per_xcd * kXcd)), dim3(256), 0, s, t);
+    };
+    static const char* ev = getenv("SNACK_V");
+    const int v = ev ? atoi(ev) : 0;
+    const int64_t n32 = (int64_t)a.rblocks * tiles;
+    if (v == 21 || (v == 0 && (n32 >= 8 * (int64_t)L->cus || a.steps == 1))) go(sample_kernel<2, 1>, 2, 1);
+    else go(sample_kernel<1, 4>, 1, 4);
+    SNACK_HIP(hipGetLastError());
+    return SNACK_OK;
+}
+
+}  // namespace snack
