@@ -498,12 +498,16 @@ snack_status canon_index_tail(snack_layer* L, hipStream_t s, bool idx16_done, bo
 {
     if (!idx16_done) SNACK_CHECK(build_idx16(L, s));
     L->vals_t_stale = false;
-    L->sample_valid = false;
     for (int i = 0; i < kTileWidths; ++i) {
         L->fwd.split[i].valid = false;
         L->tr.split[i].valid = false;
     }
     SNACK_CHECK(build_view_partitions(L, s, empty_cleared));
+    L->sample_valid = false;
+    if (L->sample_used) {
+        SNACK_CHECK(sample_index(L, s));
+        L->sample_valid = true;
+    }
     return SNACK_OK;
 }
 

@@ -128,10 +128,11 @@ struct snack_layer {
 
     // the positions in tile order and the tiles' places in it, for the dW of
     // dense enough layers by matrix instructions (sample.hip; else null),
-    // remade when the index changes
+    // made by the first call that reads it and from then on with every change of
+    // the index (so a call captured in a graph reads the present one)
     uint32_t* sample_list = nullptr;   // [cap]
     int32_t* sample_ptr = nullptr;
-    mutable bool sample_valid = false;
+    mutable bool sample_valid = false, sample_used = false;
 
     snack::View fwd;   // idx = cols
     snack::View tr;    // idx = rows_t
@@ -256,9 +257,10 @@ snack_status ckpt_transpose(const uint8_t* Q, const uint8_t* S, int fmt, int n, 
 // this size has the tile list, and whether a batch plan takes the path; the bytes
 // of the tiles' places and of the workspace; dW from Q, S and dY [B][M]
 bool sample_layer(int64_t M, int64_t K, int64_t nnz);
-bool sample_applies(const snack_layer* L, const BatchPlan& p);
+bool sample_applies(const snack_layer* L, const BatchPlan& p, bool want_dx);
 size_t sample_ptr_bytes(const snack_layer* L);
 size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p);
+snack_status sample_index(const snack_layer* L, hipStream_t s);   // the tile list of the present index
 snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
                        float* dW, void* ws, hipStream_t s);
 

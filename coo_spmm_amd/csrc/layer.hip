@@ -426,7 +426,7 @@ extern "C" snack_status snack_backward_ckpt(snack_layer* L, const uint8_t* Q, co
     if (!dW) return backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr);
     const BatchPlan p = plan_batch(B);
     SNACK_CHECK(ws_check(L, p));
-    if (sample_applies(L, p)) {
+    if (sample_applies(L, p, dX != nullptr)) {
         L->dwt_valid = false;
         SNACK_CHECK(sample_dw(L, Q, S, fmt, dY, B, dW, L->ws, s));
         return dX ? backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr) : SNACK_OK;

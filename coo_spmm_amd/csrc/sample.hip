@@ -3,17 +3,19 @@
 //   dW[k] = sum_b dY[b, r_k] x[b, c_k]
 //
 // Walking the stored positions costs every entry two operand rows of B values, so
-// past about one position in a hundred it is cheaper to compute whole tiles of
-// dY^T X on the matrix cores and keep only the stored positions.  A wavefront's
-// registers hold up to 64 x 128 cells; they go to LDS 32 rows at a time, from
-// where the stored ones are read and written to dW.  The dense product itself
+// past about one position in 64 it is cheaper to compute whole tiles of dY^T X on
+// the matrix cores and keep only the stored positions.  A wavefront's registers
+// hold 32 x 128 cells; they go to LDS 16 rows at a time, from where the stored
+// ones are read and written to dW.  (Tiles of 64 x 128, half the operand reads a
+// cell but two wavefronts a SIMD instead of four: no faster anywhere, 61.7 us
+// against 55.7 at 10000 x 10000, 90 %, 64 batch rows.)  The dense product itself
 // never leaves the CU.
 //
 // Which cells are stored comes from a list in tile order (32 rows x 128 columns a
 // tile, row-major within it), made once after every change of the index: 4 bytes
 // a position, read in whole lines and known before the product starts.  (Reading
 // each row's run of column indices instead, eight lanes a row, left a dependent
-// load behind every run longer than eight: 65 us against NEWTIME at 10000 x 10000,
+// load behind every run longer than eight: 65 us against 42 at 10000 x 10000,
 // 95 %, 64 batch rows.)
 //
 // fp32 accuracy from bf16 instructions: an fp32 number is the exact sum of three
@@ -29,7 +31,6 @@
 // bytes a lane), once, so the product's loads are whole kilobytes from L2 into
 // registers, without LDS and without barriers.
 #include "ckpt.h"
-#include <stdlib.h>
 
 namespace snack {
 namespace {
@@ -41,7 +42,8 @@ constexpr int kStep = 16;             // batch rows of one instruction
 constexpr int kCols = 128;            // columns of a tile
 constexpr int kCB = kCols / 32;
 constexpr int kCellBits = 12;         // a cell of a tile: 32 x 128
-constexpr int kSampleMaxK = 32768;    // columns at most: a slot of a 32-row panel then fits the other 20 bits
+constexpr int kSampleMaxK = 32640;    // columns at most: a slot of a 32-row panel then fits the other 20 bits,
+                                      // and the list kernel's tables 64 KB
 constexpr int kAhead = 4;             // list words a lane holds
 constexpr int kStage = 16 * kCols;    // cells a wavefront stages at once: half a tile
 constexpr int kXcd = 8;
@@ -186,16 +188,15 @@ struct SampleArgs {
     const int32_t* row_ptr;
     float* dW;
     int steps, rblocks, cblocks;
-    int panels, tiles;     // tiles of a wavefront down and across
+    int tiles;             // across; rblocks of them down
     int per_xcd;           // workgroups an XCD takes
     uint32_t a_bytes, x_bytes;
 };
 
-// RB: 32-row blocks of a wavefront's tile.  KS: wavefronts of the workgroup that
-// share a tile, each a KS-th of the batch rows; their sums are added, in wavefront
-// order, where the positions are read.
-template <int RB, int KS>
-__global__ void __launch_bounds__(256, RB == 1 ? 4 : 2) sample_kernel(SampleArgs P)
+// KS: wavefronts of the workgroup that share a tile, each a KS-th of the batch rows;
+// their sums are added, in wavefront order, where the positions are read.
+template <int KS>
+__global__ void __launch_bounds__(256, 4) sample_kernel(SampleArgs P)
 {
     __shared__ float stage[4][kStage];
     const int lane = (int)threadIdx.x & (kWave - 1);
@@ -205,32 +206,26 @@ __global__ void __launch_bounds__(256, RB == 1 ? 4 : 2) sample_kernel(SampleArgs
     // the pieces of a row's dW that neighbouring tiles write meet there
     const int64_t unit = (int64_t)(blockIdx.x % kXcd) * P.per_xcd + blockIdx.x / kXcd;
     const int64_t tile = unit * (4 / KS) + wave / KS;
-    if (tile >= (int64_t)P.panels * P.tiles) return;   // with KS > 1 the whole workgroup
-    const int panel = (int)((uint32_t)tile / (uint32_t)P.tiles);
-    const int ct = (int)((uint32_t)tile - (uint32_t)panel * (uint32_t)P.tiles);
+    const bool live = tile < (int64_t)P.rblocks * P.tiles;
+    if (KS == 1 && !live) return;
+    // with KS > 1 the workgroup's wavefronts meet at barriers: one past the end repeats the last tile and stores nothing
+    const int64_t id = live ? tile : (int64_t)P.rblocks * P.tiles - 1;
+    const int panel = (int)((uint32_t)id / (uint32_t)P.tiles);
+    const int ct = (int)((uint32_t)id - (uint32_t)panel * (uint32_t)P.tiles);
 
-    // the first positions this wavefront stores: the words ks * 64 + lane, + 64 KS, ... of each tile's list
-    int32_t p1[RB], pos[RB];
-    uint32_t word[RB][kAhead];
+    // the first positions this wavefront stores: the words ks * 64 + lane, + 64 KS, ... of the tile's list
+    const int32_t pos = P.tile_ptr[id] + ks * kWave + lane;
+    const int32_t p1 = live ? P.tile_ptr[id + 1] : 0;
+    uint32_t word[kAhead];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int rp = panel * RB + rb;
-        const bool ok = rp < P.rblocks;
-        const int64_t id = (int64_t)min(rp, P.rblocks - 1) * P.tiles + ct;
-        pos[rb] = P.tile_ptr[id] + ks * kWave + lane;
-        p1[rb] = ok ? P.tile_ptr[id + 1] : 0;
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)   // the list is padded: reads past the tile's end stay in bounds
-            word[rb][k] = P.list[pos[rb] + k * KS * kWave];
-    }
+    for (int k = 0; k < kAhead; ++k)   // the list is padded: reads past the tile's end stay in bounds
+        word[k] = P.list[pos + k * KS * kWave];
 
-    f32x16 acc[RB][kCB];
+    f32x16 acc[kCB];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
+    for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
-        for (int cb = 0; cb < kCB; ++cb)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[rb][cb][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) acc[cb][i] = 0.0f;
 
     if (ks < P.steps) {
         // Loads through buffer descriptors: the block's offset is a scalar, the lane's a constant, and a
@@ -245,21 +240,19 @@ __global__ void __launch_bounds__(256, RB == 1 ? 4 : 2) sample_kernel(SampleArgs
         auto frag_x = [&](uint32_t blk) {
             return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rx, at, (int)(blk * kFragBytes), 0));
         };
-        uint32_t a[RB], x[kCB];
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) a[rb] = (uint32_t)min(panel * RB + rb, P.rblocks - 1) * P.steps * 3;
+        const uint32_t a = (uint32_t)panel * P.steps * 3;
+        uint32_t x[kCB];
 #pragma unroll
         for (int cb = 0; cb < kCB; ++cb) x[cb] = (uint32_t)min(ct * kCB + cb, P.cblocks - 1) * P.steps;
         // one set of A registers, each refilled for the next step as soon as its products are issued, and
-        // two of X: with the sums that is what fits at two wavefronts a SIMD
-        bf16x8 fa[RB][3], fx[kCB], nx[kCB];
+        // two of X: with the sums that is what fits at four wavefronts a SIMD
+        bf16x8 fa[3], fx[kCB], nx[kCB];
 #pragma unroll
         for (int cb = 0; cb < kCB; ++cb) fx[cb] = frag_x(x[cb] + ks);
 #pragma unroll
         for (int q = 2; q >= 0; --q) {   // in the loop's order, so that its waits need not be wider
             __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) fa[rb][q] = frag_a(a[rb] + ks * 3 + q);
+            fa[q] = frag_a(a + ks * 3 + q);
         }
 #pragma unroll 1
         for (int s = ks; s < P.steps; s += KS) {
@@ -270,13 +263,9 @@ __global__ void __launch_bounds__(256, RB == 1 ? 4 : 2) sample_kernel(SampleArgs
 #pragma unroll
             for (int q = 2; q >= 0; --q) {   // the smallest part first
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-                    for (int cb = 0; cb < kCB; ++cb)
-                        acc[rb][cb] =
-                            __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[rb][q], fx[cb], acc[rb][cb], 0, 0, 0);
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) fa[rb][q] = frag_a(a[rb] + next * 3 + q);
+                for (int cb = 0; cb < kCB; ++cb)
+                    acc[cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[q], fx[cb], acc[cb], 0, 0, 0);
+                fa[q] = frag_a(a + next * 3 + q);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -296,38 +285,34 @@ __global__ void __launch_bounds__(256, RB == 1 ? 4 : 2) sample_kernel(SampleArgs
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
     };
+    float* out = P.dW + P.row_ptr[panel * 32];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        float* out = P.dW + P.row_ptr[min(panel * RB + rb, P.rblocks - 1) * 32];
+    for (int half = 0; half < 2; ++half) {
+        if (half > 0) settle();
+        // lane l holds column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4 of each 32 x 32 block
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (rb + half > 0) settle();
-            // lane l holds column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4 of each 32 x 32 block
+        for (int cb = 0; cb < kCB; ++cb)
 #pragma unroll
-            for (int cb = 0; cb < kCB; ++cb)
+            for (int i = 0; i < 8; ++i)
+                mine[(8 * (i / 4) + 4 * (lane >> 5) + (i & 3)) * kCols + cb * 32 + (lane & 31)] = acc[cb][8 * half + i];
+        settle();
+        auto put = [&](uint32_t w, int32_t e) {
+            const int cell = (int)(w & ((1u << kCellBits) - 1)) - half * kStage;
+            if (e < p1 && (uint32_t)cell < (uint32_t)kStage) {
+                float v = group[cell];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mine[(8 * (i / 4) + 4 * (lane >> 5) + (i & 3)) * kCols + cb * 32 + (lane & 31)] =
-                        acc[rb][cb][8 * half + i];
-            settle();
-            auto put = [&](uint32_t w, int32_t e) {
-                const int cell = (int)(w & ((1u << kCellBits) - 1)) - half * kStage;
-                if (e < p1[rb] && (uint32_t)cell < (uint32_t)kStage) {
-                    float v = group[cell];
-#pragma unroll
-                    for (int j = 1; j < KS; ++j) v += group[cell + j * kStage];
-                    out[w >> kCellBits] = v;
-                }
-            };
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) put(word[rb][k], pos[rb] + k * KS * kWave);
-            for (int32_t e = pos[rb] + kAhead * KS * kWave; e < p1[rb]; e += kAhead * KS * kWave) {
-                uint32_t more[kAhead];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) more[k] = P.list[e + k * KS * kWave];
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) put(more[k], e + k * KS * kWave);
+                for (int j = 1; j < KS; ++j) v += group[cell + j * kStage];
+                out[w >> kCellBits] = v;
             }
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) put(word[k], pos + k * KS * kWave);
+        for (int32_t e = pos + kAhead * KS * kWave; e < p1; e += kAhead * KS * kWave) {
+            uint32_t more[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) more[k] = P.list[e + k * KS * kWave];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) put(more[k], e + k * KS * kWave);
         }
     }
 }
@@ -336,14 +321,23 @@ inline int blocks32(int n) { return (n + 31) / 32; }
 
 }  // namespace
 
-// Where the tiles beat the walk over the positions: at least one position in 64 cells, and 16 batch rows
-// (an instruction's depth); operands below 4 GB (buffer offsets).
+// Where the tiles beat the walk over the positions, which gets its dX nearly free beside dW at up to 64
+// batch rows.  Measured (us, walk : tiles), int8:
+//   dW alone     8 rows,  10000 x 10000: 95 % 31.9 : 26.8, 98 % 18.0 : 22.2;  2500 x 2500: 95 % 12.2 : 7.4
+//               64 rows,  10000 x 10000: 95 % 88.2 : 49.1, 98 % 44.7 : 47.3;  2500 x 2500: 98 % 16.9 : 8.8
+//             1024 rows,  2500 x 2500: 98 % 46.4 : 46.8;  768 x 3072: 98 % 37.7 : 27.9, 99 % 31.8 : 28.3
+//   dX and dW   16 rows,  10000 x 10000: 95 % 47.0 : 49.8;  500 x 500: 90 % 12.1 : 14.0
+//               64 rows,  10000 x 10000: 95 % 111 : 104, 98 % 74 : 93;  500 x 500: 95 % 20.5 : 18.5
+//              200 rows,  6000 x 1500: 95 % 74.0 : 62.2, 98 % 73.7 : 56.2;  500 x 500: 95 % 17.1 : 16.4
+// Operands stay below 4 GB (buffer offsets).
 bool sample_layer(int64_t M, int64_t K, int64_t nnz) { return nnz > 0 && K <= kSampleMaxK && nnz >= M * K / 64; }
-bool sample_applies(const snack_layer* L, const BatchPlan& p)
+bool sample_applies(const snack_layer* L, const BatchPlan& p, bool want_dx)
 {
+    if (!L->sample_list) return false;
+    const bool dense = L->nnz >= (int64_t)L->M * L->K / 32;
+    if (want_dx ? p.bp <= (dense ? 16 : 64) : p.bp < (dense ? 8 : 32)) return false;
     const int64_t steps = (p.bp + kStep - 1) / kStep;
-    return L->sample_list && p.bp >= kStep && steps * 3 * blocks32(L->M) < (1ll << 32) / kFragBytes &&
-           steps * blocks32(L->K) < (1ll << 32) / kFragBytes;
+    return steps * 3 * blocks32(L->M) < (1ll << 32) / kFragBytes && steps * blocks32(L->K) < (1ll << 32) / kFragBytes;
 }
 
 size_t sample_ptr_bytes(const snack_layer* L)
@@ -353,9 +347,19 @@ size_t sample_ptr_bytes(const snack_layer* L)
 
 size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p)
 {
-    if (!sample_applies(L, p)) return 0;
+    if (!sample_applies(L, p, false)) return 0;   // where it applies beside dX, it applies alone
     const size_t steps = (size_t)(p.bp + kStep - 1) / kStep;
     return steps * kWave * sizeof(uint4) * (3 * (size_t)blocks32(L->M) + blocks32(L->K));
+}
+
+snack_status sample_index(const snack_layer* L, hipStream_t s)
+{
+    const int tiles = (L->K + kCols - 1) / kCols;
+    hipLaunchKernelGGL(sample_list_kernel, dim3((unsigned)blocks32(L->M)), dim3(256),
+                       (size_t)32 * (2 * tiles + 1) * sizeof(int32_t), s, L->row_ptr, L->cols, L->M, tiles,
+                       L->sample_list, L->sample_ptr);
+    SNACK_HIP(hipGetLastError());
+    return SNACK_OK;
 }
 
 snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
@@ -364,14 +368,12 @@ snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S,
     ProfScope prof(KC_SDDMM_DW, s);
     const int tiles = (L->K + kCols - 1) / kCols;
     if (!L->sample_valid) {
-        hipLaunchKernelGGL(sample_list_kernel, dim3((unsigned)blocks32(L->M)), dim3(256),
-                           (size_t)32 * (2 * tiles + 1) * sizeof(int32_t), s, L->row_ptr, L->cols, L->M, tiles,
-                           L->sample_list, L->sample_ptr);
-        SNACK_HIP(hipGetLastError());
+        SNACK_CHECK(sample_index(L, s));
         // a list recorded into a graph is only made when the graph runs: eager calls make their own
         hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
         SNACK_HIP(hipStreamIsCapturing(s, &cap));
         L->sample_valid = cap == hipStreamCaptureStatusNone;
+        L->sample_used = true;
     }
     SplitArgs a;
     a.dY = dY;
@@ -404,17 +406,18 @@ snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S,
     t.a_bytes = (uint32_t)a.rblocks * a.steps * 3 * kFragBytes;
     t.x_bytes = (uint32_t)a.cblocks * a.steps * kFragBytes;
     t.tiles = tiles;
-    auto go = [&](auto kern, int rb, int ks) {
-        t.panels = (a.rblocks + rb - 1) / rb;
-        const int64_t units = ((int64_t)t.panels * tiles + 4 / ks - 1) / (4 / ks);
+    auto go = [&](auto kern, int ks) {
+        const int64_t units = ((int64_t)a.rblocks * tiles + 4 / ks - 1) / (4 / ks);
         t.per_xcd = (int)((units + kXcd - 1) / kXcd);
         hipLaunchKernelGGL(kern, dim3((unsigned)(t.per_xcd * kXcd)), dim3(256), 0, s, t);
     };
-    static const char* ev = getenv("SNACK_V");
-    const int v = ev ? atoi(ev) : 0;
-    const int64_t n32 = (int64_t)a.rblocks * tiles;
-    if (v == 21 || (v == 0 && (n32 >= 8 * (int64_t)L->cus || a.steps == 1))) go(sample_kernel<2, 1>, 2, 1);
-    else go(sample_kernel<1, 4>, 1, 4);
+    // Wavefronts a tile: one where the tiles alone give every SIMD one, else two or four.  Measured with
+    // 1, 2 and 4 (us, 1024 rows): 64 tiles (500 x 500) 29.6, 18.8, 13.8; 576 tiles (768 x 3072) 35.4, 28.5,
+    // 30.5; 1580 tiles (2500 x 2500) 47.6, 51.9, 52.6.
+    const int64_t all = (int64_t)a.rblocks * tiles;
+    if (all >= 4 * (int64_t)L->cus) go(sample_kernel<1>, 1);
+    else if (all >= L->cus) go(sample_kernel<2>, 2);
+    else go(sample_kernel<4>, 4);
     SNACK_HIP(hipGetLastError());
     return SNACK_OK;
 }

@@ -285,6 +285,44 @@ def test_layer_gradients_wide():
     _layer_case(768, 3072, 23592, (1000,), "ckpt/layer/down", [O.E4M3])
 
 
+@pytest.mark.parametrize("M,K,nnz", [(6000, 900, 540000), (4100, 1200, 100000), (40, 32640, 45000), (40, 32641, 45000)])
+def test_layer_gradients_many_tiles(M, K, nnz):
+    """A wavefront a tile; long and short lists of a tile; the widest layer with tiles and one past it."""
+    _layer_case(M, K, nnz, (8, 33, 100), f"ckpt/tiles/{M}x{K}", [O.INT8])
+
+
+def test_captured_gradient_reads_the_present_index():
+    """A call captured before a drop/regrow and replayed after it."""
+    import torch
+    L = lib()
+    M, K, nnz, B, key = 300, 260, 12000, 64, "ckpt/captured"
+    rows, cols, vals = random_layer(M, K, nnz, key)
+    layer = L.SnackLayer(M, K, dev(rows), dev(cols), dev(vals), seed=4)
+    try:
+        ck, dY = L.Ckpt.pack(dev(normal((B, K), key + "/x")), L.E4M3), dev(normal((B, M), key + "/dy"))
+        dW = torch.zeros(nnz, device="cuda")
+        graphs = []
+        for warm in (False, True):       # captured as the layer's first such call, and after an eager one
+            say("capture", warm)
+            if warm:
+                layer.backward_ckpt(ck, dY, want_dx=False, dW=dW)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                layer.backward_ckpt(ck, dY, want_dx=False, dW=dW)
+            graphs.append(g)
+        for step in range(3):
+            for i, g in enumerate(graphs):
+                say("replay", step, i)
+                dW.zero_()
+                g.replay()
+                torch.cuda.synchronize()
+                assert torch.equal(dW, layer.backward_ckpt(ck, dY, want_dx=False)[1])
+            layer.prune_regrow(3000)
+    finally:
+        layer.close()
+
+
 def test_layer_gradients_follow_the_support():
     """After drop/regrow and a value change the gradients are those of the new triple."""
     import oracle
