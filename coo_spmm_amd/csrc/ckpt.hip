@@ -209,36 +209,6 @@ gelu_ckpt_bwd_kernel(const uint32_t* __restrict__ QX, const uint8_t* __restrict_
     }
 }
 
-// the checkpoint of a batch as the feature-major operand the layer's passes read:
-// xt[c * bp + b] for b < B, 0 up to bp.  A workgroup takes 64 features (two blocks)
-// of 64 rows: codes in as whole words of a row, values out as runs of a feature.
-template <int FMT>
-__global__ void __launch_bounds__(kThreads) ckpt_transpose_kernel(const uint32_t* __restrict__ Q,
-                                                                  const uint8_t* __restrict__ S, int n, int per_row,
-                                                                  int B, int bp, float* __restrict__ xt)
-{
-    __shared__ float tile[64][65];
-    const int c0 = (int)blockIdx.x * 64, b0 = (int)blockIdx.y * 64;
-    const int word = (int)threadIdx.x & 15;           // four features
-    const int blk = c0 / kCkptBlock + word / 8;
-    for (int bb = (int)threadIdx.x >> 4; bb < 64; bb += kThreads / 16) {
-        const int b = b0 + bb;
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (b < B && blk < per_row) {
-            const int64_t at = (int64_t)b * per_row + blk;
-            v = ckpt_codes4<FMT>(Q[at * 8 + (word & 7)]) * ckpt_scale(S[at]);
-        }
-        tile[bb][4 * word] = v.x;
-        tile[bb][4 * word + 1] = v.y;
-        tile[bb][4 * word + 2] = v.z;
-        tile[bb][4 * word + 3] = v.w;
-    }
-    __syncthreads();
-    const int b = b0 + ((int)threadIdx.x & 63);
-    for (int cc = (int)threadIdx.x >> 6; cc < 64; cc += kThreads / 64)
-        if (c0 + cc < n && b < bp) xt[(int64_t)(c0 + cc) * bp + b] = tile[threadIdx.x & 63][cc];
-}
-
 // rows x n as numbered blocks; false where they number 2^31 or more
 bool make_shape(int64_t rows, int64_t n, Shape* sh)
 {
@@ -269,18 +239,6 @@ snack_status common(int64_t rows, int64_t n, int32_t fmt, Shape* sh)
 }
 
 }  // namespace
-
-snack_status ckpt_transpose(const uint8_t* Q, const uint8_t* S, int fmt, int n, int B, int bp, float* xt,
-                            hipStream_t s)
-{
-    ProfScope prof(KC_TRANSPOSE, s);
-    const int per_row = (n + kCkptBlock - 1) / kCkptBlock;
-    const dim3 grid((unsigned)((n + 63) / 64), (unsigned)((bp + 63) / 64));
-    const auto k = fmt == SNACK_INT8 ? ckpt_transpose_kernel<SNACK_INT8> : ckpt_transpose_kernel<SNACK_E4M3>;
-    hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, s, (const uint32_t*)Q, S, n, per_row, B, bp, xt);
-    SNACK_HIP(hipGetLastError());
-    return SNACK_OK;
-}
 
 }  // namespace snack
 

@@ -249,20 +249,28 @@ BatchPlan plan_batch(int B);
 snack_status transpose_pad(const float* src, float* dst, int n, const float* src2, float* dst2, int n2, int B,
                            int bp, hipStream_t s);
 
-// The same copy from a checkpoint (codes Q, exponent bytes S) of src [B, n] (ckpt.hip)
-snack_status ckpt_transpose(const uint8_t* Q, const uint8_t* S, int fmt, int n, int B, int bp, float* xt,
-                            hipStream_t s);
+// What the gradient passes read, from dY [B][M] and the checkpoint (Q, S) of x
+// [B][K], in one launch (operands.hip).  Null: not wanted.
+constexpr int kSampleStep = 16;   // batch rows of one matrix instruction
+struct LayerOperands {
+    float* dyt;   // [M][bp] and [K][bp], as transpose_pad leaves them
+    float* xt;
+    void* a;      // the instruction operands of sample_dw
+    void* x;
+};
+snack_status layer_operands(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
+                            int bp, const LayerOperands& out, hipStream_t s);
 
 // dW from a checkpoint by matrix instructions (sample.hip): whether a layer of
 // this size has the tile list, and whether a batch plan takes the path; the bytes
-// of the tiles' places and of the workspace; dW from Q, S and dY [B][M]
+// of the tiles' places and of the operands (dY's first, x's after a_bytes); dW
+// from the operands
 bool sample_layer(int64_t M, int64_t K, int64_t nnz);
 bool sample_applies(const snack_layer* L, const BatchPlan& p, bool want_dx);
 size_t sample_ptr_bytes(const snack_layer* L);
-size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p);
+size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p, size_t* a_bytes = nullptr);
 snack_status sample_index(const snack_layer* L, hipStream_t s);   // the tile list of the present index
-snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
-                       float* dW, void* ws, hipStream_t s);
+snack_status sample_dw(const snack_layer* L, const void* a, const void* x, int B, float* dW, hipStream_t s);
 
 // Whether every kernel of a forward (fwd) or backward (dx, dw requested) pass
 // can take the caller's batch-major [B][n] arrays directly, so no

@@ -55,9 +55,9 @@ size_t ws_need(const snack_layer* L, const BatchPlan& p)
 {
     const size_t a = (((size_t)L->K * p.bp * 4) + 255) & ~(size_t)255;
     const size_t b = (((size_t)L->M * p.bp * 4) + 255) & ~(size_t)255;
-    // the operands of the dW from a checkpoint are used up before a pass writes anything else here
-    const size_t rest = a + b + tile_part_bytes(L, p) + wide_dw_bytes(L, p), sample = sample_ws_bytes(L, p);
-    return rest > sample ? rest : sample;
+    // the operands of the dW from a checkpoint are used up before a pass writes partial sums in their place
+    const size_t part = tile_part_bytes(L, p) + wide_dw_bytes(L, p), sample = sample_ws_bytes(L, p);
+    return a + b + (part > sample ? part : sample);
 }
 
 // grow the workspace to hold plan p (never shrinks); the new buffer is
@@ -426,18 +426,25 @@ extern "C" snack_status snack_backward_ckpt(snack_layer* L, const uint8_t* Q, co
     if (!dW) return backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr);
     const BatchPlan p = plan_batch(B);
     SNACK_CHECK(ws_check(L, p));
+    // the copies in the workspace, where this plan's passes read them
+    const bool copies = p.bp > 1 && !spmm_batch_major(L, p, false, dX != nullptr, true);
     if (sample_applies(L, p, dX != nullptr)) {
+        const bool dx_copies = dX && p.bp > 1 && !spmm_batch_major(L, p, false, true, false);
+        size_t a_bytes = 0;
+        (void)sample_ws_bytes(L, p, &a_bytes);
+        char* a = (char*)ws_part(L, p);
         L->dwt_valid = false;
-        SNACK_CHECK(sample_dw(L, Q, S, fmt, dY, B, dW, L->ws, s));
-        return dX ? backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr) : SNACK_OK;
+        SNACK_CHECK(layer_operands(L, Q, S, fmt, dY, B, p.bp, {dx_copies ? ws_dy(L, p) : nullptr, nullptr, a, a + a_bytes}, s));
+        SNACK_CHECK(sample_dw(L, a, a + a_bytes, B, dW, s));
+        return dX ? backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr, false, dx_copies) : SNACK_OK;
     }
-    // X as the passes of this plan read it, in the workspace's place for its feature-major copy
-    if (p.bp == 1 || spmm_batch_major(L, p, false, dX != nullptr, true)) {
-        SNACK_CHECK(snack_ckpt_unpack(Q, S, B, L->K, fmt, ws_x(L), SNACK_F32, stream));
-        return backward_impl(L, ws_x(L), dY, dX, dW, B, s, nullptr);
+    if (copies) {
+        SNACK_CHECK(layer_operands(L, Q, S, fmt, dY, B, p.bp, {ws_dy(L, p), ws_x(L), nullptr, nullptr}, s));
+        return backward_impl(L, ws_x(L), dY, dX, dW, B, s, nullptr, true, true);
     }
-    SNACK_CHECK(ckpt_transpose(Q, S, fmt, L->K, B, p.bp, ws_x(L), s));
-    return backward_impl(L, ws_x(L), dY, dX, dW, B, s, nullptr, true);
+    // batch-major passes: x in the workspace's place for its feature-major copy
+    SNACK_CHECK(snack_ckpt_unpack(Q, S, B, L->K, fmt, ws_x(L), SNACK_F32, stream));
+    return backward_impl(L, ws_x(L), dY, dX, dW, B, s, nullptr);
 }
 
 namespace {

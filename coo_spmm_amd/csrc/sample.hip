@@ -26,10 +26,10 @@
 // multiply-adds.  Against a checkpoint this costs half of what two fp32
 // operands would (six products).
 //
-// split_operands_kernel writes both operands in the order in which the matrix
-// instruction takes them (32 rows or columns x 16 batch rows, a kilobyte, 16
-// bytes a lane), once, so the product's loads are whole kilobytes from L2 into
-// registers, without LDS and without barriers.
+// Both operands come in the order in which the matrix instruction takes them (32
+// rows or columns x 16 batch rows, a kilobyte, 16 bytes a lane; operands.hip), so
+// the product's loads are whole kilobytes from L2 into registers, without LDS and
+// without barriers.
 #include "ckpt.h"
 
 namespace snack {
@@ -38,7 +38,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kStep = 16;             // batch rows of one instruction
+constexpr int kStep = kSampleStep;
 constexpr int kCols = 128;            // columns of a tile
 constexpr int kCB = kCols / 32;
 constexpr int kCellBits = 12;         // a cell of a tile: 32 x 128
@@ -48,74 +48,6 @@ constexpr int kAhead = 4;             // list words a lane holds
 constexpr int kStage = 16 * kCols;    // cells a wavefront stages at once: half a tile
 constexpr int kXcd = 8;
 constexpr int kFragBytes = kWave * 16;   // one instruction's operand
-
-// the three bf16 parts of x (hi + mid + lo = x); an infinity or NaN is all in the first
-__device__ inline void split3(float x, uint16_t& hi, uint16_t& mid, uint16_t& lo)
-{
-    const uint32_t b = __float_as_uint(x);
-    const bool fin = (b & 0x7F800000u) != 0x7F800000u;
-    const float r1 = x - __uint_as_float(b & 0xFFFF0000u);
-    const uint32_t b1 = fin ? __float_as_uint(r1) : 0u;
-    const float r2 = __uint_as_float(b1) - __uint_as_float(b1 & 0xFFFF0000u);
-    const uint32_t nan = (b & 0x7FFFFFFFu) > 0x7F800000u ? 0x40u : 0u;
-    hi = (uint16_t)((b >> 16) | nan);
-    mid = (uint16_t)(b1 >> 16);
-    lo = (uint16_t)(__float_as_uint(r2) >> 16);
-}
-
-struct SplitArgs {
-    const float* dY;      // [B][M]
-    const uint8_t* Q;     // [B][32 per_row]
-    const uint8_t* S;     // [B][per_row]
-    uint4* A;             // [row blocks][steps][3][64]
-    uint4* X;             // [column blocks][steps][64]
-    int M, K, B, per_row, steps, rblocks, cblocks;
-};
-
-// A wavefront makes one block: lane l holds row (column) l % 32 and the eight
-// batch rows 8 (l / 32) ... of a step; rows, columns and batch rows past the
-// end are zeros.
-template <int FMT>
-__global__ void __launch_bounds__(256) split_operands_kernel(SplitArgs P)
-{
-    const int lane = (int)threadIdx.x & (kWave - 1);
-    const int64_t w = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-    const int64_t na = (int64_t)P.rblocks * P.steps, nx = (int64_t)P.cblocks * P.steps;
-    if (w >= na + nx) return;
-    const bool first = w < na;
-    const int64_t v = first ? w : w - na;
-    // neighbouring wavefronts take neighbouring rows (columns) of the same batch rows
-    const int nb = first ? P.rblocks : P.cblocks;
-    const int step = (int)(v / nb), blk = (int)(v - (int64_t)step * nb);
-    const int c = blk * 32 + (lane & 31);
-    const int b0 = step * kStep + 8 * (lane >> 5);
-    if (first) {
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (c < P.M && b0 + j < P.B) ? P.dY[(int64_t)(b0 + j) * P.M + c] : 0.0f;
-        uint16_t part[3][8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split3(x[j], part[0][j], part[1][j], part[2][j]);
-        uint4* out = P.A + (((int64_t)blk * P.steps + step) * 3) * kWave + lane;
-#pragma unroll
-        for (int q = 0; q < 3; ++q)
-            out[q * kWave] = make_uint4(part[q][0] | part[q][1] << 16, part[q][2] | part[q][3] << 16,
-                                        part[q][4] | part[q][5] << 16, part[q][6] | part[q][7] << 16);
-    } else {
-        uint16_t x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = 0;
-            if (c < P.K && b0 + j < P.B) {
-                const int64_t row = (int64_t)(b0 + j) * P.per_row + blk;
-                const f32x4 v4 = ckpt_codes4<FMT>(P.Q[row * kCkptBlock + (lane & 31)]);
-                x[j] = bf16_bits(v4.x * ckpt_scale(P.S[row]));
-            }
-        }
-        P.X[((int64_t)blk * P.steps + step) * kWave + lane] =
-            make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
-    }
-}
 
 // The tile list of one panel of 32 rows by one workgroup.  A panel's positions are
 // one run of the canonical order; the list holds the same run in tile order:
@@ -345,11 +277,12 @@ size_t sample_ptr_bytes(const snack_layer* L)
     return ((size_t)((L->K + kCols - 1) / kCols) * blocks32(L->M) + 1) * sizeof(int32_t);
 }
 
-size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p)
+size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p, size_t* a_bytes)
 {
     if (!sample_applies(L, p, false)) return 0;   // where it applies beside dX, it applies alone
-    const size_t steps = (size_t)(p.bp + kStep - 1) / kStep;
-    return steps * kWave * sizeof(uint4) * (3 * (size_t)blocks32(L->M) + blocks32(L->K));
+    const size_t step = (size_t)((p.bp + kStep - 1) / kStep) * kFragBytes, a = 3 * step * blocks32(L->M);
+    if (a_bytes) *a_bytes = a;
+    return a + step * blocks32(L->K);
 }
 
 snack_status sample_index(const snack_layer* L, hipStream_t s)
@@ -362,11 +295,9 @@ snack_status sample_index(const snack_layer* L, hipStream_t s)
     return SNACK_OK;
 }
 
-snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S, int fmt, const float* dY, int B,
-                       float* dW, void* ws, hipStream_t s)
+snack_status sample_dw(const snack_layer* L, const void* a, const void* x, int B, float* dW, hipStream_t s)
 {
     ProfScope prof(KC_SDDMM_DW, s);
-    const int tiles = (L->K + kCols - 1) / kCols;
     if (!L->sample_valid) {
         SNACK_CHECK(sample_index(L, s));
         // a list recorded into a graph is only made when the graph runs: eager calls make their own
@@ -375,48 +306,31 @@ snack_status sample_dw(const snack_layer* L, const uint8_t* Q, const uint8_t* S,
         L->sample_valid = cap == hipStreamCaptureStatusNone;
         L->sample_used = true;
     }
-    SplitArgs a;
-    a.dY = dY;
-    a.Q = Q;
-    a.S = S;
-    a.M = L->M;
-    a.K = L->K;
-    a.B = B;
-    a.per_row = blocks32(L->K);
-    a.steps = (B + kStep - 1) / kStep;
-    a.rblocks = blocks32(L->M);
-    a.cblocks = blocks32(L->K);
-    a.A = (uint4*)ws;
-    a.X = a.A + (size_t)a.rblocks * a.steps * 3 * kWave;
-    const int64_t waves = (int64_t)(a.rblocks + a.cblocks) * a.steps;
-    const auto split = fmt == SNACK_INT8 ? split_operands_kernel<SNACK_INT8> : split_operands_kernel<SNACK_E4M3>;
-    hipLaunchKernelGGL(split, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a);
-    SNACK_HIP(hipGetLastError());
-
     SampleArgs t;
-    t.A = a.A;
-    t.X = a.X;
+    t.A = (const uint4*)a;
+    t.X = (const uint4*)x;
     t.list = L->sample_list;
     t.tile_ptr = L->sample_ptr;
     t.row_ptr = L->row_ptr;
     t.dW = dW;
-    t.steps = a.steps;
-    t.rblocks = a.rblocks;
-    t.cblocks = a.cblocks;
-    t.a_bytes = (uint32_t)a.rblocks * a.steps * 3 * kFragBytes;
-    t.x_bytes = (uint32_t)a.cblocks * a.steps * kFragBytes;
-    t.tiles = tiles;
+    t.steps = (B + kStep - 1) / kStep;
+    t.rblocks = blocks32(L->M);
+    t.cblocks = blocks32(L->K);
+    t.a_bytes = (uint32_t)t.rblocks * t.steps * 3 * kFragBytes;
+    t.x_bytes = (uint32_t)t.cblocks * t.steps * kFragBytes;
+    t.tiles = (L->K + kCols - 1) / kCols;
     auto go = [&](auto kern, int ks) {
-        const int64_t units = ((int64_t)a.rblocks * tiles + 4 / ks - 1) / (4 / ks);
+        const int64_t units = ((int64_t)t.rblocks * t.tiles + 4 / ks - 1) / (4 / ks);
         t.per_xcd = (int)((units + kXcd - 1) / kXcd);
         hipLaunchKernelGGL(kern, dim3((unsigned)(t.per_xcd * kXcd)), dim3(256), 0, s, t);
     };
-    // Wavefronts a tile: one where the tiles alone give every SIMD one, else two or four.  Measured with
-    // 1, 2 and 4 (us, 1024 rows): 64 tiles (500 x 500) 29.6, 18.8, 13.8; 576 tiles (768 x 3072) 35.4, 28.5,
-    // 30.5; 1580 tiles (2500 x 2500) 47.6, 51.9, 52.6.
-    const int64_t all = (int64_t)a.rblocks * tiles;
-    if (all >= 4 * (int64_t)L->cus) go(sample_kernel<1>, 1);
-    else if (all >= L->cus) go(sample_kernel<2>, 2);
+    // Wavefronts a tile: one where the tiles alone give every SIMD more than one, else two or four.  Measured
+    // with 1, 2 and 4 (us, 1024 rows, with the operands' launch): 64 tiles (500 x 500) 29.6, 18.8, 13.8;
+    // 576 tiles (3072 x 768) 36.6, 31.2, 28.7; 1008 tiles (2000 x 2000) 37.7, 32.5, 34.0;
+    // 1580 tiles (2500 x 2500) 47.6, 51.9, 52.6.
+    const int64_t all = (int64_t)t.rblocks * t.tiles;
+    if (all >= 5 * (int64_t)L->cus) go(sample_kernel<1>, 1);
+    else if (all >= 3 * (int64_t)L->cus) go(sample_kernel<2>, 2);
     else go(sample_kernel<4>, 4);
     SNACK_HIP(hipGetLastError());
     return SNACK_OK;
