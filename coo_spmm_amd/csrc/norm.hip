@@ -27,6 +27,11 @@ constexpr int kRowMax = 1024 * 4 * kChunks;      // longest row of one workgroup
 constexpr int kLongThreads = 1024;               // workgroup of the rows past it
 constexpr int kBwdGroups = 512;                  // most workgroups (and partial rows) of the gradient
 constexpr int kColThreads = 256;                 // column pass of rows past kRowMax
+// Outputs of a forward call past this many bytes, the size of the last-level cache, are stored past the caches:
+// nothing of them would still be there for whoever reads them.  Measured (us, cached : past them): 8192 x 5000,
+// 288 MB, 115 : 105 alone; with a reader of y behind it 32768 x 2000, 459 MB, 231 : 221, but 16384 x 2000,
+// 229 MB, 107 : 113 and 4096 x 2000, 57 MB, 26.0 : 28.2.
+constexpr int64_t kStreamBytes = 256ll << 20;
 constexpr int kSumCols = 32, kSumRows = 32;      // final sum: columns and row strides of a workgroup
 
 // x added over the lanes of a wavefront, the same tree in every lane
@@ -76,21 +81,24 @@ __device__ inline f32x4 load4(const uint16_t* __restrict__ p, int64_t left)
     }
     return f32x4{bf16_value(h.x), bf16_value(h.y), bf16_value(h.z), bf16_value(h.w)};
 }
-__device__ inline void store4(float* __restrict__ p, f32x4 v, int64_t left)
+// stream: past the caches (a value that is the same for the whole launch)
+__device__ inline void store4(float* __restrict__ p, f32x4 v, int64_t left, bool stream = false)
 {
     if (left >= 4) {
-        *reinterpret_cast<f32x4u*>(p) = v;
+        if (stream) __builtin_nontemporal_store(v, reinterpret_cast<f32x4u*>(p));
+        else *reinterpret_cast<f32x4u*>(p) = v;
         return;
     }
     if (left > 0) p[0] = v.x;
     if (left > 1) p[1] = v.y;
     if (left > 2) p[2] = v.z;
 }
-__device__ inline void store4(uint16_t* __restrict__ p, f32x4 v, int64_t left)
+__device__ inline void store4(uint16_t* __restrict__ p, f32x4 v, int64_t left, bool stream = false)
 {
     const u16x4u h = {bf16_bits(v.x), bf16_bits(v.y), bf16_bits(v.z), bf16_bits(v.w)};
     if (left >= 4) {
-        *reinterpret_cast<u16x4u*>(p) = h;
+        if (stream) __builtin_nontemporal_store(h, reinterpret_cast<u16x4u*>(p));
+        else *reinterpret_cast<u16x4u*>(p) = h;
         return;
     }
     if (left > 0) p[0] = h.x;
@@ -110,6 +118,7 @@ struct FwdArgs {
     uint8_t* S;
     int64_t rows, n, per_row;   // per_row: blocks of a row
     float eps;
+    bool stream;                // h and y past the caches
 };
 
 // h of four features: x + residual, rounded to the stream's type
@@ -131,7 +140,7 @@ template <int QF>
 __device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t at, int64_t left, f32x4 h, float r)
 {
     const f32x4 y = h * r * load4(A.gain + f, left);
-    if (A.Y) store4(A.Y + at, y, left);
+    if (A.Y) store4(A.Y + at, y, left, A.stream);
     if constexpr (QF != SNACK_F32) {
         const int64_t blk = row * A.per_row + f / kCkptBlock;
         ckpt_store<QF>(y, (uint32_t*)(A.Q + blk * kCkptBlock) + ((f / 4) & 7), A.S + blk, (int)((f / 4) & 7));
@@ -159,7 +168,7 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int64_t f = 4 * (t + (int64_t)i * nt);
-        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h[i], A.n - f);
+        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h[i], A.n - f, A.stream);
         ss += dot4(h[i], h[i]);
     }
     ss = WG ? group_sum(ss, part) : wave_sum(ss);
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(FwdArgs A)
     float ss = 0.0f;
     for (int64_t f = 4 * (int64_t)threadIdx.x; f < A.n; f += 4 * kLongThreads) {
         const f32x4 h = hidden4<HF>(A, base + f, A.n - f);
-        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h, A.n - f);
+        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h, A.n - f, A.stream);
         ss += dot4(h, h);
     }
     ss = group_sum(ss, part);
@@ -415,7 +424,8 @@ extern "C" snack_status snack_rmsnorm_fwd(const float* X, const void* R, int32_t
         return SNACK_ERR_INVALID_ARG;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     ProfScope prof(KC_NORM, s);
-    const FwdArgs A{X, R, gain, H, Y, rstd, Q, S, rows, n, (n + kCkptBlock - 1) / kCkptBlock, eps};
+    const int64_t out = rows * n * ((H ? (int64_t)ha : 0) + (Y ? 4 : 0) + (Q ? 1 : 0));
+    const FwdArgs A{X, R, gain, H, Y, rstd, Q, S, rows, n, (n + kCkptBlock - 1) / kCkptBlock, eps, out > kStreamBytes};
     const int qf = Q ? q_fmt : (int)SNACK_F32;
     if (h_fmt == SNACK_BF16 && R) launch_fwd<SNACK_BF16>(A, qf, s);
     else launch_fwd<SNACK_F32>(A, qf, s);

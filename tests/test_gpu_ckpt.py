@@ -164,6 +164,24 @@ def test_norm_forward(rows, n, hf):
     _close(host(y), yr, 37 * O.U32 * np.abs(yr), "y without residual")
 
 
+@pytest.mark.parametrize("rows,n", [(8000, 4999), (2400, 17001), (44000, 900)])
+def test_norm_forward_large(rows, n):
+    """Outputs past the caches are stored another way: the same bits as in pieces that are not."""
+    import torch
+    L = lib()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, gain = torch.randn(rows, n, device="cuda", generator=g), torch.randn(n, device="cuda", generator=g)
+    res = torch.randn(rows, n, device="cuda", generator=g).bfloat16()
+    say("norm large", rows, n)
+    h, y, rstd, ck = L.rmsnorm_fwd(x, gain, 1e-6, residual=res, q_format=L.E4M3)
+    assert rows * n * 7 > 256 << 20
+    for a in range(0, rows, 1000):
+        b = min(rows, a + 1000)
+        h2, y2, r2, c2 = L.rmsnorm_fwd(x[a:b], gain, 1e-6, residual=res[a:b], q_format=L.E4M3)
+        for t, u in ((h, h2), (y, y2), (rstd, r2), (ck.q, c2.q), (ck.s, c2.s)):
+            assert torch.equal(t[a:b], u), a
+
+
 @pytest.mark.parametrize("hf", ["f32", "bf16", "int8", "e4m3"])
 @pytest.mark.parametrize("rows,n", SHAPES + [(2100, 96), (600, 1100)])
 def test_norm_backward(rows, n, hf):
