@@ -7,15 +7,21 @@
 //   dx = rstd (w - xh mean(w xh)) + dR,  xh = h rstd,  w = dY gain
 //   dgain = sum over rows of dY xh
 //
-// Both directions are one pass over HBM: a row stays in registers between its
-// sum and its outputs.  Rows of up to 1024 features take one wavefront each
-// (the sum never leaves it), longer ones a workgroup of as many wavefronts as
-// give every thread at most four groups of four features; rows past 16384
-// features, which no longer fit, are read twice.  Features are dealt to threads
-// so that eight neighbouring lanes always hold one 32-feature block.
-// dgain: every workgroup adds up its own rows' terms in registers, in row order,
-// and writes one row of partial sums; a second kernel adds the partial rows in a
-// fixed tree.  No atomics, so the result does not depend on timing.
+// Both directions are one pass over HBM, which bounds them: a row stays in
+// registers between its sum and its outputs.  Rows of up to 1024 features take one
+// wavefront each (the sum never leaves it), longer ones a workgroup of as many
+// wavefronts as give every thread at most four groups of four features; rows past
+// 16384 features, which no longer fit, and rows of less than four are read twice.
+// Features are dealt to threads so that eight neighbouring lanes always hold one
+// 32-feature block.  All of a row's loads are in flight before the first is used
+// (read4).  dgain: every workgroup adds up its own rows' terms in registers, in row
+// order, and writes one row of partial sums; a second kernel adds the partial rows
+// in a fixed tree.  No atomics, so the result does not depend on timing.
+//
+// Measured (a copy of 1 GiB runs at 5.2 TB/s): forward 8192 x 5000, bf16 residual,
+// e4m3 checkpoint, 534 MB in 109 us (4.9 TB/s); 1 x 768 in 2.7 us (a launch).
+// Gradient 3333 x 4999, fp32 h, 266 MB in 44 us and 4.9 us for the partial rows;
+// 10000 x 1500 from an int8 checkpoint, 195 MB in 40 us with both.
 #include "ckpt.h"
 
 namespace snack {
@@ -25,7 +31,9 @@ constexpr int kChunks = 4;                       // groups of four features a th
 constexpr int kWaveRow = kWave * 4 * kChunks;    // longest row of one wavefront
 constexpr int kRowMax = 1024 * 4 * kChunks;      // longest row of one workgroup
 constexpr int kLongThreads = 1024;               // workgroup of the rows past it
-constexpr int kBwdGroups = 512;                  // most workgroups (and partial rows) of the gradient
+constexpr int kCus = 256;                        // compute units
+constexpr int kBwdWaves = 10;                    // wavefronts a unit of the gradient, and most workgroups
+constexpr int kBwdPerCu = 4;
 constexpr int kColThreads = 256;                 // column pass of rows past kRowMax
 // Outputs of a forward call past this many bytes, the size of the last-level cache, are stored past the caches:
 // nothing of them would still be there for whoever reads them.  Measured (us, cached : past them): 8192 x 5000,
@@ -51,6 +59,7 @@ __device__ inline float group_sum(float x, float* part)
     if ((threadIdx.x & (kWave - 1)) == 0) part[w] = x;
     __syncthreads();
     float s = 0.0f;
+#pragma unroll 4
     for (int i = 0; i < nw; ++i) s += part[i];
     return s;
 }
@@ -60,7 +69,8 @@ struct HType { using T = float; };
 template <>
 struct HType<SNACK_BF16> { using T = uint16_t; };
 
-__device__ inline f32x4 load4(const float* __restrict__ p, int64_t left)
+// Four features from p, of which the first `left` exist (the others are 0).
+__device__ inline f32x4 load4(const float* __restrict__ p, int left)
 {
     if (left >= 4) return *reinterpret_cast<const f32x4u*>(p);
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -69,7 +79,12 @@ __device__ inline f32x4 load4(const float* __restrict__ p, int64_t left)
     if (left > 2) v.z = p[2];
     return v;
 }
-__device__ inline f32x4 load4(const uint16_t* __restrict__ p, int64_t left)
+__device__ inline f32x4 value4(f32x4 v) { return v; }
+__device__ inline f32x4 value4(u16x4u h)
+{
+    return f32x4{bf16_value(h.x), bf16_value(h.y), bf16_value(h.z), bf16_value(h.w)};
+}
+__device__ inline f32x4 load4(const uint16_t* __restrict__ p, int left)
 {
     u16x4u h = {0, 0, 0, 0};
     if (left >= 4) {
@@ -79,10 +94,34 @@ __device__ inline f32x4 load4(const uint16_t* __restrict__ p, int64_t left)
         if (left > 1) h.y = p[1];
         if (left > 2) h.z = p[2];
     }
-    return f32x4{bf16_value(h.x), bf16_value(h.y), bf16_value(h.z), bf16_value(h.w)};
+    return value4(h);
 }
+
+// The same from a row of n >= 4 features, in two steps without a branch round the load: read4 takes the last four
+// of the row where fewer are left, kept4 brings them in place.  A thread's loads are then all issued before the
+// first is waited for (with a branch round each, its conversion holds the next load back: a row of 1100 features
+// of a checkpoint took 3.7 us in place of 1.7).
+// The row's address is a scalar and a lane's offset in it 32 unsigned bits: one register an access.
+__device__ inline const char* at_bytes(const void* row, uint32_t bytes) { return (const char*)row + bytes; }
+__device__ inline char* at_bytes(void* row, uint32_t bytes) { return (char*)row + bytes; }
+__device__ inline f32x4 read4(const float* __restrict__ row, int f, int n)
+{
+    return *reinterpret_cast<const f32x4u*>(at_bytes(row, 4u * (uint32_t)min(f, n - 4)));
+}
+__device__ inline u16x4u read4(const uint16_t* __restrict__ row, int f, int n)
+{
+    return *reinterpret_cast<const u16x4u*>(at_bytes(row, 2u * (uint32_t)min(f, n - 4)));
+}
+__device__ inline f32x4 kept4(f32x4 v, int left)
+{
+    if (left >= 4) return v;
+    return f32x4{left > 2 ? v.y : left > 1 ? v.z : left > 0 ? v.w : 0.0f, left > 2 ? v.z : left > 1 ? v.w : 0.0f,
+                 left > 2 ? v.w : 0.0f, 0.0f};
+}
+__device__ inline f32x4 kept4(u16x4u h, int left) { return kept4(value4(h), left); }
+
 // stream: past the caches (a value that is the same for the whole launch)
-__device__ inline void store4(float* __restrict__ p, f32x4 v, int64_t left, bool stream = false)
+__device__ inline void store4(float* __restrict__ p, f32x4 v, int left, bool stream = false)
 {
     if (left >= 4) {
         if (stream) __builtin_nontemporal_store(v, reinterpret_cast<f32x4u*>(p));
@@ -93,7 +132,7 @@ __device__ inline void store4(float* __restrict__ p, f32x4 v, int64_t left, bool
     if (left > 1) p[1] = v.y;
     if (left > 2) p[2] = v.z;
 }
-__device__ inline void store4(uint16_t* __restrict__ p, f32x4 v, int64_t left, bool stream = false)
+__device__ inline void store4(uint16_t* __restrict__ p, f32x4 v, int left, bool stream = false)
 {
     const u16x4u h = {bf16_bits(v.x), bf16_bits(v.y), bf16_bits(v.z), bf16_bits(v.w)};
     if (left >= 4) {
@@ -123,23 +162,25 @@ struct FwdArgs {
 
 // h of four features: x + residual, rounded to the stream's type
 template <int HF>
-__device__ inline f32x4 hidden4(const FwdArgs& A, int64_t at, int64_t left)
+__device__ inline f32x4 hidden4(f32x4 x, f32x4 res)
 {
-    f32x4 h = load4(A.X + at, left);
-    if (A.R) {
-        h += load4(reinterpret_cast<const typename HType<HF>::T*>(A.R) + at, left);
-        if constexpr (HF == SNACK_BF16)
-            h = f32x4{bf16_value(bf16_bits(h.x)), bf16_value(bf16_bits(h.y)), bf16_value(bf16_bits(h.z)),
-                      bf16_value(bf16_bits(h.w))};
-    }
-    return h;
+    const f32x4 h = x + res;
+    if constexpr (HF != SNACK_BF16) return h;
+    return f32x4{bf16_value(bf16_bits(h.x)), bf16_value(bf16_bits(h.y)), bf16_value(bf16_bits(h.z)),
+                 bf16_value(bf16_bits(h.w))};
+}
+template <int HF>
+__device__ inline f32x4 hidden4(const FwdArgs& A, int64_t at, int left)
+{
+    const f32x4 x = load4(A.X + at, left);
+    return A.R ? hidden4<HF>(x, load4((const typename HType<HF>::T*)A.R + at, left)) : x;
 }
 
 // y of four features and what is kept of it
 template <int QF>
-__device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t at, int64_t left, f32x4 h, float r)
+__device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t at, int left, f32x4 h, f32x4 g, float r)
 {
-    const f32x4 y = h * r * load4(A.gain + f, left);
+    const f32x4 y = h * r * g;
     if (A.Y) store4(A.Y + at, y, left, A.stream);
     if constexpr (QF != SNACK_F32) {
         const int64_t blk = row * A.per_row + f / kCkptBlock;
@@ -157,18 +198,33 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
     if (row >= A.rows) return;   // never with WG
     const int t = WG ? (int)threadIdx.x : (int)threadIdx.x & (kWave - 1);
     const int nt = WG ? (int)blockDim.x : kWave;
+    const int n = (int)A.n;
     const int64_t base = row * A.n;
-    f32x4 h[kChunks];
-    float ss = 0.0f;
+    f32x4 h[kChunks], g[kChunks];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int64_t f = 4 * (t + (int64_t)i * nt);
-        h[i] = hidden4<HF>(A, base + f, A.n - f);
+    for (int i = 0; i < kChunks; ++i) h[i] = read4(A.X + base, 4 * (t + i * nt), n);
+    if (A.R) {
+        decltype(read4((const T*)nullptr, 0, 0)) res[kChunks];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) res[i] = read4((const T*)A.R + base, 4 * (t + i * nt), n);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) g[i] = read4(A.gain, 4 * (t + i * nt), n);
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) h[i] = hidden4<HF>(h[i], value4(res[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) g[i] = read4(A.gain, 4 * (t + i * nt), n);
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int64_t f = 4 * (t + (int64_t)i * nt);
-        if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h[i], A.n - f, A.stream);
+        h[i] = kept4(h[i], n - 4 * (t + i * nt));
+        g[i] = kept4(g[i], n - 4 * (t + i * nt));
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int f = 4 * (t + i * nt);
+        if (A.H) store4((T*)A.H + base + f, h[i], n - f, A.stream);
         ss += dot4(h[i], h[i]);
     }
     ss = WG ? group_sum(ss, part) : wave_sum(ss);
@@ -176,9 +232,9 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
     if (t == 0) A.rstd[row] = r;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int64_t f = 4 * (t + (int64_t)i * nt);
+        const int f = 4 * (t + i * nt);
         // whole blocks: the eight lanes of a row's last block stay together
-        if ((f & ~(int64_t)(kCkptBlock - 1)) < A.n) finish4<QF>(A, row, f, base + f, A.n - f, h[i], r);
+        if ((f & ~(kCkptBlock - 1)) < n) finish4<QF>(A, row, f, base + f, n - f, h[i], g[i], r);
     }
 }
 
@@ -199,7 +255,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(FwdArgs A)
     const float r = 1.0f / sqrtf(ss / (float)A.n + A.eps);
     if (threadIdx.x == 0) A.rstd[row] = r;
     for (int64_t f = 4 * (int64_t)threadIdx.x; (f & ~(int64_t)(kCkptBlock - 1)) < A.n; f += 4 * kLongThreads)
-        finish4<QF>(A, row, f, base + f, A.n - f, hidden4<HF>(A, base + f, A.n - f), r);
+        finish4<QF>(A, row, f, base + f, A.n - f, hidden4<HF>(A, base + f, A.n - f), load4(A.gain + f, A.n - f), r);
 }
 
 struct BwdArgs {
@@ -211,62 +267,114 @@ struct BwdArgs {
     const float* dR;      // gradient that reaches h directly, or null
     float* dX;
     float* part;          // [gridDim.x][n] partial sums of dgain, or null
-    float* mean;          // [rows] mean(w xh) (rows past kRowMax)
+    float* mean;          // [rows] mean(w xh) (long_rows)
     int64_t rows, n, per_row;
 };
 
+// Four features of one row of h, from feature f, in the same two steps: h and hs are the row's (its codes and
+// exponent bytes for a checkpoint, whose codes past the n-th are bytes, but no values).
 template <int HF>
-__device__ inline f32x4 kept4(const BwdArgs& A, int64_t row, int64_t f, int64_t left)
+struct Kept {
+    decltype(read4((const typename HType<HF>::T*)nullptr, 0, 0)) v;
+    __device__ inline void read(const void* __restrict__ h, const uint8_t* __restrict__, int f, int n)
+    {
+        v = read4((const typename HType<HF>::T*)h, f, n);
+    }
+    __device__ inline f32x4 value(int left) const { return kept4(v, left); }
+};
+template <int HF>
+struct KeptCodes {
+    uint32_t w, s;
+    __device__ inline void read(const void* __restrict__ h, const uint8_t* __restrict__ hs, int f, int n)
+    {
+        const uint32_t at = (uint32_t)min(f, (n - 1) & ~3);
+        w = *reinterpret_cast<const uint32_t*>(at_bytes(h, at));
+        s = *(const uint8_t*)at_bytes(hs, at / kCkptBlock);
+    }
+    __device__ inline f32x4 value(int left) const
+    {
+        f32x4 v = ckpt_codes4<HF>(w) * ckpt_scale(s);
+        if (left >= 4) return v;
+        return f32x4{left > 0 ? v.x : 0.0f, left > 1 ? v.y : 0.0f, left > 2 ? v.z : 0.0f, 0.0f};
+    }
+};
+template <>
+struct Kept<SNACK_INT8> : KeptCodes<SNACK_INT8> {};
+template <>
+struct Kept<SNACK_E4M3> : KeptCodes<SNACK_E4M3> {};
+
+// the same for rows of any length
+template <int HF>
+__device__ inline f32x4 hidden_row4(const void* __restrict__ h, const uint8_t* __restrict__ hs, int f, int n)
 {
     if constexpr (HF == SNACK_INT8 || HF == SNACK_E4M3) {
-        if (left <= 0) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t blk = row * A.per_row + f / kCkptBlock;
-        const uint32_t w = ((const uint32_t*)A.H)[blk * (kCkptBlock / 4) + ((f / 4) & 7)];
-        f32x4 v = ckpt_codes4<HF>(w) * ckpt_scale(A.HS[blk]);
-        // codes past the row's end are not values
-        if (left < 2) v.y = 0.0f;
-        if (left < 3) v.z = 0.0f;
-        if (left < 4) v.w = 0.0f;
-        return v;
+        Kept<HF> k;
+        k.read(h, hs, f, n);
+        return k.value(n - f);
     } else {
-        return load4(reinterpret_cast<const typename HType<HF>::T*>(A.H) + row * A.n + f, left);
+        return load4((const typename HType<HF>::T*)h + f, n - f);
     }
 }
-
-template <int HF, bool WG>
-__global__ void __launch_bounds__(WG ? 1024 : 256) norm_bwd_kernel(BwdArgs A)
+template <int HF>
+__device__ inline const void* kept_row(const BwdArgs& A, int64_t row)
 {
+    if constexpr (HF == SNACK_INT8 || HF == SNACK_E4M3) return (const uint8_t*)A.H + row * A.per_row * kCkptBlock;
+    else return (const typename HType<HF>::T*)A.H + row * A.n;
+}
+
+// T: most threads of a workgroup: 256 for a wavefront a row, else of the workgroup that takes one.  With 1024
+// there are 128 registers a thread, and the gain lies in LDS.
+template <int HF, int T>
+__global__ void __launch_bounds__(T) norm_bwd_kernel(BwdArgs A)
+{
+    constexpr bool WG = T > 256, GAIN_LDS = T > 512;
+    __shared__ f32x4 gain[GAIN_LDS ? kChunks * T : 1];
     __shared__ float part[32];
     __shared__ float gsum[WG ? 1 : 3 * kWaveRow];
-    const int wave = (int)threadIdx.x / kWave;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int t = WG ? (int)threadIdx.x : (int)threadIdx.x & (kWave - 1);
     const int nt = WG ? (int)blockDim.x : kWave;
+    const int n = (int)A.n;
     const int64_t step = WG ? (int64_t)gridDim.x : (int64_t)gridDim.x * 4;
     const float inv_n = 1.0f / (float)A.n;
     f32x4 g[kChunks], acc[kChunks];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int64_t f = 4 * (t + (int64_t)i * nt);
-        g[i] = load4(A.gain + f, A.n - f);
+        const int f = 4 * (t + i * nt);
+        g[i] = kept4(read4(A.gain, f, n), n - f);
+        if constexpr (GAIN_LDS) gain[t + i * T] = g[i];   // read by the thread that wrote it
         acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     int flip = 0;
     for (int64_t row = WG ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave; row < A.rows; row += step) {
         const float r = A.rstd[row];
-        const int64_t base = row * A.n;
-        f32x4 xh[kChunks], w[kChunks];
+        const void* h = kept_row<HF>(A, row);
+        const uint8_t* hs = A.HS + row * A.per_row;
+        const float* dy = A.dY + row * A.n;
+        const float* dr = A.dR ? A.dR + row * A.n : nullptr;
+        float* dx = A.dX + row * A.n;
+        int n = (int)A.n;
+        asm volatile("" : "+s"(n));   // keeps the offsets and tails of the row from being held across rows
+        Kept<HF> kept[kChunks];
+        f32x4 xh[kChunks], w[kChunks], e[kChunks];
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int64_t f = 4 * (t + (int64_t)i * nt);
-            xh[i] = kept4<HF>(A, row, f, A.n - f);
-            w[i] = load4(A.dY + base + f, A.n - f);
+            const int f = 4 * (t + i * nt);
+            kept[i].read(h, hs, f, n);
+            w[i] = read4(dy, f, n);
+        }
+        if (dr) {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) e[i] = read4(dr, 4 * (t + i * nt), n);
         }
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            xh[i] *= r;
+            const int left = n - 4 * (t + i * nt);
+            xh[i] = kept[i].value(left) * r;
+            w[i] = kept4(w[i], left);
             acc[i] += w[i] * xh[i];
-            w[i] *= g[i];
+            w[i] *= GAIN_LDS ? gain[t + i * T] : g[i];
             dot += dot4(w[i], xh[i]);
         }
         dot = WG ? group_sum(dot, part + 16 * flip) : wave_sum(dot);
@@ -274,10 +382,10 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_bwd_kernel(BwdArgs A)
         const float c = dot * inv_n;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
-            const int64_t f = 4 * (t + (int64_t)i * nt);
+            const int f = 4 * (t + i * nt);
             f32x4 o = (w[i] - xh[i] * c) * r;
-            if (A.dR) o += load4(A.dR + base + f, A.n - f);
-            store4(A.dX + base + f, o, A.n - f);
+            if (dr) o += kept4(e[i], n - f);
+            store4((float*)at_bytes(dx, 4u * (uint32_t)f), o, n - f);
         }
     }
     if (!A.part) return;
@@ -297,8 +405,8 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_bwd_kernel(BwdArgs A)
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-        const int64_t f = 4 * (t + (int64_t)i * nt);
-        store4(A.part + (int64_t)blockIdx.x * A.n + f, acc[i], A.n - f);
+        const int f = 4 * (t + i * nt);
+        store4(A.part + (int64_t)blockIdx.x * A.n + f, acc[i], n - f);
     }
 }
 
@@ -308,10 +416,14 @@ __global__ void __launch_bounds__(kLongThreads) norm_bwd_mean_kernel(BwdArgs A)
 {
     __shared__ float part[16];
     const int64_t row = blockIdx.x, base = row * A.n;
+    const void* h = kept_row<HF>(A, row);
+    const uint8_t* hs = A.HS + row * A.per_row;
     const float r = A.rstd[row];
     float dot = 0.0f;
-    for (int64_t f = 4 * (int64_t)threadIdx.x; f < A.n; f += 4 * kLongThreads)
-        dot += dot4(load4(A.dY + base + f, A.n - f) * load4(A.gain + f, A.n - f), kept4<HF>(A, row, f, A.n - f) * r);
+    for (int64_t f = 4 * (int64_t)threadIdx.x; f < A.n; f += 4 * kLongThreads) {
+        const int left = (int)(A.n - f);
+        dot += dot4(load4(A.dY + base + f, left) * load4(A.gain + f, left), hidden_row4<HF>(h, hs, (int)f, (int)A.n) * r);
+    }
     dot = group_sum(dot, part);
     if (threadIdx.x == 0) A.mean[row] = dot / (float)A.n;
 }
@@ -320,15 +432,16 @@ __global__ void __launch_bounds__(kLongThreads) norm_bwd_mean_kernel(BwdArgs A)
 template <int HF>
 __global__ void __launch_bounds__(kColThreads) norm_bwd_cols_kernel(BwdArgs A)
 {
-    const int64_t f = 4 * ((int64_t)blockIdx.y * kColThreads + threadIdx.x);
-    const int64_t left = A.n - f;
-    if (left <= 0) return;
+    const int64_t at0 = 4 * ((int64_t)blockIdx.y * kColThreads + threadIdx.x);
+    if (at0 >= A.n) return;
+    const int f = (int)at0, left = (int)(A.n - at0);
     const f32x4 g = load4(A.gain + f, left);
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int64_t row = blockIdx.x; row < A.rows; row += gridDim.x) {
         const float r = A.rstd[row], c = A.mean[row];
         const int64_t at = row * A.n + f;
-        const f32x4 xh = kept4<HF>(A, row, f, left) * r, d = load4(A.dY + at, left);
+        const f32x4 xh = hidden_row4<HF>(kept_row<HF>(A, row), A.HS + row * A.per_row, f, (int)A.n) * r;
+        const f32x4 d = load4(A.dY + at, left);
         acc += d * xh;
         f32x4 o = (d * g - xh * c) * r;
         if (A.dR) o += load4(A.dR + at, left);
@@ -357,16 +470,28 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) part_sum_kernel(const flo
     }
 }
 
+// rows that do not stay in registers, and those too short for read4
+bool long_rows(int64_t n) { return n < 4 || n > kRowMax; }
+
 // threads of a workgroup that takes a row of n features (kWaveRow < n <= kRowMax)
 int row_threads(int64_t n) { return kWave * (int)((n + kWaveRow - 1) / kWaveRow); }
 
-// workgroups of the gradient, one partial row of dgain each.  A fixed count (two
-// a CU) rather than one a row: at 3333 x 4999 the partial rows are then a
-// seventh of dY's bytes instead of all of them.
+// Workgroups of the gradient, one partial row of dgain each: a fixed number of them rather than one a row (at
+// 3333 x 4999 the partial rows are then a seventh of dY's bytes instead of all of them), the same number on every
+// compute unit, of about ten wavefronts.  Measured with 1, 2, 3 and 4 a unit (us, int8 h): 1500 features (2
+// wavefronts) 86, 50, 41, 40; 3000 (3) 52, 40, 41, 42; 4999 (5) 52, 44.5, 50, 53; 9000 (9) 52, 57, 61, 67;
+// 16000 (16) 49, 55, 62, 68.
 int bwd_groups(int64_t rows, int64_t n)
 {
-    const int64_t g = n <= kWaveRow ? (rows + 3) / 4 : rows;
-    return (int)(g < kBwdGroups ? g : kBwdGroups);
+    int64_t most = kCus, g = rows;
+    if (n <= kWaveRow) {
+        g = (rows + 3) / 4;
+        most *= n > kWaveRow / 2 ? kBwdWaves / 4 : kBwdPerCu;   // 20000 x 200: 25.8 us with two, 20.9 with four
+    } else if (n <= kRowMax) {
+        const int per_cu = kBwdWaves / (row_threads(n) / kWave);
+        most *= per_cu < 1 ? 1 : per_cu > kBwdPerCu ? kBwdPerCu : per_cu;
+    }
+    return (int)(g < most ? g : most);
 }
 
 bool bad_size(int64_t rows, int64_t n) { return n >= (1ll << 31) - kCkptBlock || rows >= (1ll << 31); }
@@ -375,12 +500,12 @@ inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<ui
 template <int HF, int QF>
 void launch_fwd(const FwdArgs& A, hipStream_t s)
 {
-    if (A.n <= kWaveRow)
-        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, false>), dim3((unsigned)((A.rows + 3) / 4)), dim3(256), 0, s, A);
-    else if (A.n <= kRowMax)
-        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, true>), dim3((unsigned)A.rows), dim3(row_threads(A.n)), 0, s, A);
-    else
+    if (long_rows(A.n))
         hipLaunchKernelGGL((norm_fwd_long_kernel<HF, QF>), dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
+    else if (A.n <= kWaveRow)
+        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, false>), dim3((unsigned)((A.rows + 3) / 4)), dim3(256), 0, s, A);
+    else
+        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, true>), dim3((unsigned)A.rows), dim3(row_threads(A.n)), 0, s, A);
 }
 template <int HF>
 void launch_fwd(const FwdArgs& A, int q_fmt, hipStream_t s)
@@ -393,14 +518,16 @@ void launch_fwd(const FwdArgs& A, int q_fmt, hipStream_t s)
 template <int HF>
 void launch_bwd(const BwdArgs& A, int groups, hipStream_t s)
 {
-    if (A.n <= kWaveRow) {
-        hipLaunchKernelGGL((norm_bwd_kernel<HF, false>), dim3((unsigned)groups), dim3(256), 0, s, A);
-    } else if (A.n <= kRowMax) {
-        hipLaunchKernelGGL((norm_bwd_kernel<HF, true>), dim3((unsigned)groups), dim3(row_threads(A.n)), 0, s, A);
-    } else {
+    if (long_rows(A.n)) {
         hipLaunchKernelGGL(norm_bwd_mean_kernel<HF>, dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
         const unsigned cols = (unsigned)((A.n + 4 * kColThreads - 1) / (4 * kColThreads));
         hipLaunchKernelGGL(norm_bwd_cols_kernel<HF>, dim3((unsigned)groups, cols), dim3(kColThreads), 0, s, A);
+    } else if (A.n <= kWaveRow) {
+        hipLaunchKernelGGL((norm_bwd_kernel<HF, 256>), dim3((unsigned)groups), dim3(256), 0, s, A);
+    } else {
+        const int threads = row_threads(A.n);
+        const auto k = threads <= 512 ? norm_bwd_kernel<HF, 512> : norm_bwd_kernel<HF, 1024>;
+        hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(threads), 0, s, A);
     }
 }
 
@@ -437,7 +564,7 @@ extern "C" snack_status snack_rmsnorm_bwd_work(int64_t rows, int64_t n, int64_t*
 {
     if (!bytes || rows < 0 || n < 1) return SNACK_ERR_INVALID_ARG;
     if (bad_size(rows, n)) return SNACK_ERR_UNSUPPORTED;
-    *bytes = 4 * ((int64_t)bwd_groups(rows, n) * n + (n > kRowMax ? rows : 0));
+    *bytes = 4 * ((int64_t)bwd_groups(rows, n) * n + (long_rows(n) ? rows : 0));
     return SNACK_OK;
 }
 
@@ -456,7 +583,7 @@ extern "C" snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int3
         if (misaligned(H, ha) || misaligned(gain, 4) || misaligned(rstd, 4) || misaligned(dY, 4) ||
             misaligned(dR, 4) || misaligned(dX, 4))
             return SNACK_ERR_INVALID_ARG;
-        if (dgain || n > kRowMax) {
+        if (dgain || long_rows(n)) {
             if (!work || misaligned(work, 4)) return SNACK_ERR_INVALID_ARG;
             if (work_bytes < need) return SNACK_ERR_WORKSPACE;
         }
@@ -467,7 +594,7 @@ extern "C" snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int3
     ProfScope prof(KC_NORM, s);
     const int groups = bwd_groups(rows, n);
     float* mean = (float*)work;
-    float* part = (float*)work + (n > kRowMax ? rows : 0);
+    float* part = (float*)work + (long_rows(n) ? rows : 0);
     if (rows > 0) {
         const BwdArgs A{H, HS, gain, rstd, dY, dR, dX, dgain ? part : nullptr, mean, rows, n,
                         (n + kCkptBlock - 1) / kCkptBlock};

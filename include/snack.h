@@ -386,7 +386,7 @@ snack_status snack_rmsnorm_fwd(const float* X, const void* R, int32_t h_fmt, con
  *   dX       device float[rows, n];  dgain device float[n], or NULL.
  *   work     device scratch of snack_rmsnorm_bwd_work bytes, used within the
  *            call (SNACK_ERR_WORKSPACE when work_bytes is less); may be NULL
- *            where dgain is NULL and n <= 16384.
+ *            where dgain is NULL and 4 <= n <= 16384.
  */
 snack_status snack_rmsnorm_bwd_work(int64_t rows, int64_t n, int64_t* bytes);
 snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int32_t h_fmt, const float* gain, const float* rstd,
