@@ -12,6 +12,7 @@ PyTorch is used only for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -311,6 +312,7 @@ def snack_rmsnorm_fwd(X, R, h_fmt, gain, eps, H, Y, rstd, q_fmt=F32, Q=None, S=N
                                   q_fmt, _ptr(Q), _ptr(S), _stream(stream)), "snack_rmsnorm_fwd")
 
 
+@functools.lru_cache(maxsize=256)   # a function of the shape alone
 def snack_rmsnorm_bwd_work(rows, n):
     b = i64()
     _check(_lib.snack_rmsnorm_bwd_work(rows, n, ctypes.byref(b)), "snack_rmsnorm_bwd_work")

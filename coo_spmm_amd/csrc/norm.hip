@@ -16,7 +16,8 @@
 // 32-feature block.  All of a row's loads are in flight before the first is used
 // (read4).  dgain: every workgroup adds up its own rows' terms in registers, in row
 // order, and writes one row of partial sums; a second kernel adds the partial rows
-// in a fixed tree.  No atomics, so the result does not depend on timing.
+// in a fixed tree (for few rows, workgroups of their own add up columns in the same
+// launch).  No atomics, so the result does not depend on timing.
 //
 // Measured (a copy of 1 GiB runs at 5.2 TB/s): forward 8192 x 5000, bf16 residual,
 // e4m3 checkpoint, 534 MB in 109 us (4.9 TB/s); 1 x 768 in 2.7 us (a launch).
@@ -34,6 +35,7 @@ constexpr int kLongThreads = 1024;               // workgroup of the rows past i
 constexpr int kCus = 256;                        // compute units
 constexpr int kBwdWaves = 10;                    // wavefronts a unit of the gradient, and most workgroups
 constexpr int kBwdPerCu = 4;
+constexpr int kGainLanes = 4;                    // lanes of a row in the sum of dgain beside the rows
 constexpr int kColThreads = 256;                 // column pass of rows past kRowMax
 // Outputs of a forward call past this many bytes, the size of the last-level cache, are stored past the caches:
 // nothing of them would still be there for whoever reads them.  Measured (us, cached : past them): 8192 x 5000,
@@ -269,6 +271,8 @@ struct BwdArgs {
     float* part;          // [gridDim.x][n] partial sums of dgain, or null
     float* mean;          // [rows] mean(w xh) (long_rows)
     int64_t rows, n, per_row;
+    float* dgain;         // written here by the workgroups past `groups`, or null
+    int groups;           // workgroups that take rows
 };
 
 // Four features of one row of h, from feature f, in the same two steps: h and hs are the row's (its codes and
@@ -322,12 +326,57 @@ __device__ inline const void* kept_row(const BwdArgs& A, int64_t row)
     else return (const typename HType<HF>::T*)A.H + row * A.n;
 }
 
+// dgain of 4 kGainLanes features by one workgroup: kGainLanes lanes a row, then the rows' sums in a fixed tree.  It
+// needs no row's mean, so it runs beside the rows' workgroups.
+template <int HF>
+__device__ inline void gain_block(const BwdArgs& A, int block)
+{
+    constexpr int kDeep = 8;                     // rows a lane has in flight
+    __shared__ f32x4 sums[16][kGainLanes];
+    const int n = (int)A.n, f = 4 * (block * kGainLanes + (int)threadIdx.x % kGainLanes), left = n - f;
+    const int r0 = (int)threadIdx.x / kGainLanes, step = (int)blockDim.x / kGainLanes;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t row = r0; row < A.rows; row += (int64_t)kDeep * step) {
+        Kept<HF> kept[kDeep];
+        f32x4 d[kDeep];
+        float r[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int64_t at = row + (int64_t)k * step < A.rows ? row + (int64_t)k * step : A.rows - 1;
+            kept[k].read(kept_row<HF>(A, at), A.HS + at * A.per_row, f, n);
+            d[k] = read4(A.dY + at * A.n, f, n);
+            r[k] = A.rstd[at];
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+            if (row + (int64_t)k * step < A.rows) acc += kept4(d[k], left) * (kept[k].value(left) * r[k]);
+    }
+#pragma unroll
+    for (int m = kGainLanes; m < kWave; m <<= 1) {
+        acc.x += __shfl_xor(acc.x, m, kWave);
+        acc.y += __shfl_xor(acc.y, m, kWave);
+        acc.z += __shfl_xor(acc.z, m, kWave);
+        acc.w += __shfl_xor(acc.w, m, kWave);
+    }
+    const int lane = (int)threadIdx.x & (kWave - 1), nw = (int)blockDim.x / kWave;
+    if (lane < kGainLanes) sums[(int)threadIdx.x / kWave][lane] = acc;
+    __syncthreads();
+    if (threadIdx.x >= kGainLanes) return;
+    acc = sums[0][lane];
+    for (int w = 1; w < nw; ++w) acc += sums[w][lane];
+    store4(A.dgain + f, acc, left);
+}
+
 // T: most threads of a workgroup: 256 for a wavefront a row, else of the workgroup that takes one.  With 1024
 // there are 128 registers a thread, and the gain lies in LDS.
 template <int HF, int T>
 __global__ void __launch_bounds__(T) norm_bwd_kernel(BwdArgs A)
 {
     constexpr bool WG = T > 256, GAIN_LDS = T > 512;
+    if ((int)blockIdx.x >= A.groups) {
+        gain_block<HF>(A, (int)blockIdx.x - A.groups);
+        return;
+    }
     __shared__ f32x4 gain[GAIN_LDS ? kChunks * T : 1];
     __shared__ float part[32];
     __shared__ float gsum[WG ? 1 : 3 * kWaveRow];
@@ -335,7 +384,7 @@ __global__ void __launch_bounds__(T) norm_bwd_kernel(BwdArgs A)
     const int t = WG ? (int)threadIdx.x : (int)threadIdx.x & (kWave - 1);
     const int nt = WG ? (int)blockDim.x : kWave;
     const int n = (int)A.n;
-    const int64_t step = WG ? (int64_t)gridDim.x : (int64_t)gridDim.x * 4;
+    const int64_t step = WG ? (int64_t)A.groups : (int64_t)A.groups * 4;
     const float inv_n = 1.0f / (float)A.n;
     f32x4 g[kChunks], acc[kChunks];
 #pragma unroll
@@ -494,6 +543,12 @@ int bwd_groups(int64_t rows, int64_t n)
     return (int)(g < most ? g : most);
 }
 
+// Whether dgain is summed beside the rows in the same launch, which reads dY and h twice and walks all rows in every
+// workgroup, instead of from partial rows.  Measured (us on the GPU, partial rows : beside, int8 h): 256 x 768 6.2 : 3.5,
+// 1024 x 768 7.2 : 8.2 (13.2 : 10.7 called in turn, where the host's second launch counts), 1536 x 768 9.9 : 10.3,
+// 1024 x 1500 13.8 : 11.5, 2048 x 1500 15.8 : 18.9, 256 x 4999 11.7 : 10.0, 512 x 4999 15.6 : 17.7.
+bool gain_beside(int64_t rows, int64_t n) { return rows > 0 && rows <= 1024 && !long_rows(n) && rows * n <= 3 << 19; }
+
 bool bad_size(int64_t rows, int64_t n) { return n >= (1ll << 31) - kCkptBlock || rows >= (1ll << 31); }
 inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
@@ -516,18 +571,19 @@ void launch_fwd(const FwdArgs& A, int q_fmt, hipStream_t s)
 }
 
 template <int HF>
-void launch_bwd(const BwdArgs& A, int groups, hipStream_t s)
+void launch_bwd(const BwdArgs& A, hipStream_t s)
 {
+    const unsigned grid = (unsigned)A.groups + (A.dgain ? (unsigned)((A.n + 4 * kGainLanes - 1) / (4 * kGainLanes)) : 0u);
     if (long_rows(A.n)) {
         hipLaunchKernelGGL(norm_bwd_mean_kernel<HF>, dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
         const unsigned cols = (unsigned)((A.n + 4 * kColThreads - 1) / (4 * kColThreads));
-        hipLaunchKernelGGL(norm_bwd_cols_kernel<HF>, dim3((unsigned)groups, cols), dim3(kColThreads), 0, s, A);
+        hipLaunchKernelGGL(norm_bwd_cols_kernel<HF>, dim3((unsigned)A.groups, cols), dim3(kColThreads), 0, s, A);
     } else if (A.n <= kWaveRow) {
-        hipLaunchKernelGGL((norm_bwd_kernel<HF, 256>), dim3((unsigned)groups), dim3(256), 0, s, A);
+        hipLaunchKernelGGL((norm_bwd_kernel<HF, 256>), dim3(grid), dim3(256), 0, s, A);
     } else {
         const int threads = row_threads(A.n);
         const auto k = threads <= 512 ? norm_bwd_kernel<HF, 512> : norm_bwd_kernel<HF, 1024>;
-        hipLaunchKernelGGL(k, dim3((unsigned)groups), dim3(threads), 0, s, A);
+        hipLaunchKernelGGL(k, dim3(grid), dim3(threads), 0, s, A);
     }
 }
 
@@ -593,20 +649,21 @@ extern "C" snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int3
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     ProfScope prof(KC_NORM, s);
     const int groups = bwd_groups(rows, n);
+    const bool beside = gain_beside(rows, n);
     float* mean = (float*)work;
     float* part = (float*)work + (long_rows(n) ? rows : 0);
     if (rows > 0) {
-        const BwdArgs A{H, HS, gain, rstd, dY, dR, dX, dgain ? part : nullptr, mean, rows, n,
-                        (n + kCkptBlock - 1) / kCkptBlock};
+        const BwdArgs A{H, HS, gain, rstd, dY, dR, dX, dgain && !beside ? part : nullptr, mean, rows, n,
+                        (n + kCkptBlock - 1) / kCkptBlock, beside ? dgain : nullptr, groups};
         switch (h_fmt) {
-        case SNACK_F32: launch_bwd<SNACK_F32>(A, groups, s); break;
-        case SNACK_BF16: launch_bwd<SNACK_BF16>(A, groups, s); break;
-        case SNACK_INT8: launch_bwd<SNACK_INT8>(A, groups, s); break;
-        default: launch_bwd<SNACK_E4M3>(A, groups, s); break;
+        case SNACK_F32: launch_bwd<SNACK_F32>(A, s); break;
+        case SNACK_BF16: launch_bwd<SNACK_BF16>(A, s); break;
+        case SNACK_INT8: launch_bwd<SNACK_INT8>(A, s); break;
+        default: launch_bwd<SNACK_E4M3>(A, s); break;
         }
         SNACK_HIP(hipGetLastError());
     }
-    if (dgain) {
+    if (dgain && !beside) {
         // no rows: no partial rows, and the sum over none of them is 0
         hipLaunchKernelGGL(part_sum_kernel, dim3((unsigned)((n + kSumCols - 1) / kSumCols)),
                            dim3(kSumCols * kSumRows), 0, s, part, groups, n, dgain);
