@@ -409,7 +409,11 @@ snack_status snack_gelu_ckpt_bwd(const uint8_t* QX, const uint8_t* SX, const flo
  * snack_backward with the forward's input read from its checkpoint Q, S of
  * [B, K] in fmt: dX = dY W, and dW[k] = sum_b dY[b, r_k] x[b, c_k] with x the
  * values the checkpoint stands for.  dX, dW, B, the workspace and the refusals
- * as there.
+ * as there; sums in fp32.  A NaN or an infinity reaches the dW of its own row of
+ * W (from dY) or its own column (from x) only, where it gives a NaN or an
+ * infinity.  dY below 2^-109 in magnitude may lose its last bits in dW.
+ * A call captured in a graph is captured again after a drop/regrow; its dW, but
+ * not its dX, is right without that.
  */
 snack_status snack_backward_ckpt(snack_layer* layer, const uint8_t* Q, const uint8_t* S, int32_t fmt, const float* dY,
                                  float* dX, float* dW, int32_t B, snack_stream stream);

@@ -309,6 +309,11 @@ def test_layer_gradients_many_tiles(M, K, nnz):
     _layer_case(M, K, nnz, (8, 33, 100), f"ckpt/tiles/{M}x{K}", [O.INT8])
 
 
+def test_layer_gradients_short_rows():
+    """Wide batches over rows of about a dozen positions: runs of four that lie in one row, that do not, and a tail."""
+    _layer_case(3000, 900, 35003, (65, 300), "ckpt/short", [O.E4M3])
+
+
 def test_captured_gradient_reads_the_present_index():
     """A call captured before a drop/regrow and replayed after it."""
     import torch
@@ -361,6 +366,61 @@ def test_layer_gradients_follow_the_support():
                 assert_close("dW", host(dW), *oracle.backward_dw(M, K, r, c, xv, dY))
                 layer.sgd_step(dW, 0.01)
             layer.prune_regrow(3000)
+    finally:
+        layer.close()
+
+
+@pytest.mark.parametrize("how", ["random", "gradient", "rows"])
+def test_layer_gradients_after_every_regrow(how):
+    """The tile list follows each kind of drop/regrow."""
+    import oracle
+    L = lib()
+    M, K, nnz, B, key = 150, 400, 6000, 70, "ckpt/kinds"
+    rows, cols, vals = random_layer(M, K, nnz, key)
+    layer = L.SnackLayer(M, K, dev(rows), dev(cols), dev(vals), seed=5, max_batch=B)
+    try:
+        X, dY = normal((B, K), key + "/X"), normal((B, M), key + "/dY")
+        ck = L.Ckpt.pack(dev(X), O.INT8)
+        xv = O.unpack(host(ck.q), host(ck.s), O.INT8, K).astype(np.float32)
+        for step in range(3):
+            say("kinds", how, step)
+            dX, dW = layer.backward_ckpt(ck, dev(dY))
+            r, c, v = (host(t) for t in layer.export())
+            assert_close("dX", host(dX), *oracle.backward_dx(M, K, r, c, v, dY))
+            assert_close("dW", host(dW), *oracle.backward_dw(M, K, r, c, xv, dY))
+            if how == "random":
+                layer.prune_regrow(1500)
+            elif how == "gradient":
+                layer.prune_regrow_grad(1500, dev(X), dev(dY))
+            else:
+                layer.prune_regrow_rows(1, 4)
+    finally:
+        layer.close()
+
+
+@pytest.mark.parametrize("B", [3, 20, 64, 130])
+def test_layer_gradients_non_finite(B):
+    """A NaN or an infinity of dY reaches its own row's dW, one of x its own column's; the rest is as without."""
+    import oracle
+    L = lib()
+    M, K, nnz, key = 150, 200, 6000, "ckpt/nonfinite"
+    rows, cols, vals = random_layer(M, K, nnz, key)
+    layer = L.SnackLayer(M, K, dev(rows), dev(cols), dev(vals), max_batch=B)
+    try:
+        X, dY = normal((B, K), f"{key}/X/{B}"), normal((B, M), f"{key}/dY/{B}")
+        X[0, 40] = np.nan                                 # its block of 32 columns reads as NaN
+        clean = L.Ckpt.pack(dev(np.nan_to_num(X)), O.E4M3)
+        xv = O.unpack(host(clean.q), host(clean.s), O.E4M3, K).astype(np.float32)
+        r, c, _ = (host(t) for t in layer.export())
+        want, mag = oracle.backward_dw(M, K, r, c, xv, dY)
+        dY[1, 7], dY[2, 9] = np.nan, np.inf
+        ck = L.Ckpt.pack(dev(X), O.E4M3)
+        bad = (r == 7) | (r == 9) | ((c >= 32) & (c < 64))
+        for want_dx in (False, True):
+            say("non finite", B, want_dx)
+            dW = host(layer.backward_ckpt(ck, dev(dY), want_dx=want_dx)[1])
+            assert not np.isfinite(dW[bad]).any()
+            assert_close("dW", dW[~bad], want[~bad], mag[~bad])
     finally:
         layer.close()
 
