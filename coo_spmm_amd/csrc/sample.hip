@@ -254,20 +254,22 @@ inline int blocks32(int n) { return (n + 31) / 32; }
 }  // namespace
 
 // Where the tiles beat the walk over the positions, which gets its dX nearly free beside dW at up to 64
-// batch rows.  Measured (us, walk : tiles), int8:
-//   dW alone     8 rows,  10000 x 10000: 95 % 31.9 : 26.8, 98 % 18.0 : 22.2;  2500 x 2500: 95 % 12.2 : 7.4
-//               64 rows,  10000 x 10000: 95 % 88.2 : 49.1, 98 % 44.7 : 47.3;  2500 x 2500: 98 % 16.9 : 8.8
-//             1024 rows,  2500 x 2500: 98 % 46.4 : 46.8;  768 x 3072: 98 % 37.7 : 27.9, 99 % 31.8 : 28.3
-//   dX and dW   16 rows,  10000 x 10000: 95 % 47.0 : 49.8;  500 x 500: 90 % 12.1 : 14.0
-//               64 rows,  10000 x 10000: 95 % 111 : 104, 98 % 74 : 93;  500 x 500: 95 % 20.5 : 18.5
-//              200 rows,  6000 x 1500: 95 % 74.0 : 62.2, 98 % 73.7 : 56.2;  500 x 500: 95 % 17.1 : 16.4
+// batch rows (so there only large layers gain).  Measured (us a call, walk : tiles), int8:
+//   dW alone     8 rows,  10000 x 10000: 95 % 28.8 : 25.0, 98 % 14.6 : 21.7;  6000 x 1500, 95 %: 9.5 : 7.4
+//               64 rows,  10000 x 10000: 95 % 83.7 : 46.0, 98 % 39.4 : 43.6;  2500 x 2500, 98 %: 13.0 : 8.6
+//             1024 rows,  2500 x 2500, 98 %: 46.4 : 46.8;  768 x 3072: 98 % 37.7 : 27.9, 99 % 31.8 : 28.3
+//   dX and dW   16 rows,  10000 x 10000: 90 % 65.3 : 58.8, 95 % 43.1 : 45.5;  2500 x 2500, 95 %: 14.4 : 15.4
+//               64 rows,  10000 x 10000: 95 % 105.9 : 91.3, 98 % 69.3 : 80.7;  2500 x 2500, 95 %: 27.1 : 23.8;
+//                         6000 x 1500: 90 % 41.4 : 38.3, 95 % 33.2 : 34.1;  3072 x 768: 90 % 19.9 : 21.8
+//              128 rows,  3072 x 768: 90 % 23.6 : 20.1, 98 % 20.4 : 19.3;  2500 x 2500: 90 % 49.4 : 35.8, 98 % 21.0 : 22.4
 // Operands stay below 4 GB (buffer offsets).
+constexpr int64_t kSampleBesideDx = 300000;   // positions at least, at up to 64 rows
 bool sample_layer(int64_t M, int64_t K, int64_t nnz) { return nnz > 0 && K <= kSampleMaxK && nnz >= M * K / 64; }
 bool sample_applies(const snack_layer* L, const BatchPlan& p, bool want_dx)
 {
     if (!L->sample_list) return false;
     const bool dense = L->nnz >= (int64_t)L->M * L->K / 32;
-    if (want_dx ? p.bp <= (dense ? 16 : 64) : p.bp < (dense ? 8 : 32)) return false;
+    if (want_dx ? p.bp <= (dense && L->nnz >= kSampleBesideDx ? 16 : 64) : p.bp < (dense ? 8 : 32)) return false;
     const int64_t steps = (p.bp + kStep - 1) / kStep;
     return steps * 3 * blocks32(L->M) < (1ll << 32) / kFragBytes && steps * blocks32(L->K) < (1ll << 32) / kFragBytes;
 }
