@@ -46,6 +46,7 @@ constexpr int kSampleMaxK = 32640;    // columns at most: a slot of a 32-row pan
                                       // and the list kernel's tables 64 KB
 constexpr int kAhead = 4;             // list words a lane holds
 constexpr int kStage = 16 * kCols;    // cells a wavefront stages at once: half a tile
+constexpr int kListThreads = 1024;    // workgroup of a panel's list
 constexpr int kXcd = 8;
 constexpr int kFragBytes = kWave * 16;   // one instruction's operand
 
@@ -53,8 +54,9 @@ constexpr int kFragBytes = kWave * 16;   // one instruction's operand
 // one run of the canonical order; the list holds the same run in tile order:
 // list[i] = (slot - panel's first slot) << 12 | row in panel * 128 + column in tile, and
 // tile_ptr[panel * tiles + t] the place of tile t's first.  Every entry's place follows from
-// where its row enters its tile, so nothing is counted by atomics.
-__global__ void __launch_bounds__(256) sample_list_kernel(const int32_t* __restrict__ ptr,
+// where its row enters its tile, so nothing is counted by atomics.  Bound by the latency of a row's
+// loads: two rows a wavefront (10000 x 10000, 95 %: 38 us; 66 with eight).
+__global__ void __launch_bounds__(kListThreads) sample_list_kernel(const int32_t* __restrict__ ptr,
                                                           const int32_t* __restrict__ cols, int M, int tiles,
                                                           uint32_t* __restrict__ list, int32_t* __restrict__ tile_ptr)
 {
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(256) sample_list_kernel(const int32_t* __restr
     const int w = tiles + 1;
     int32_t* place = at + 32 * w;
     const int32_t base = ptr[r0];
-    for (int r = wave; r < 32; r += 4) {
+    for (int r = wave; r < 32; r += kListThreads / kWave) {
         const int32_t lo = r < nr ? ptr[r0 + r] : ptr[M], hi = r < nr ? ptr[r0 + r + 1] : ptr[M];
         for (int32_t e = lo + lane; e < hi; e += kWave) {
             const int t = cols[e] / kCols, before = e > lo ? cols[e - 1] / kCols : -1;
@@ -75,7 +77,7 @@ __global__ void __launch_bounds__(256) sample_list_kernel(const int32_t* __restr
     }
     __syncthreads();
     // a tile's entries before each row, then (one wavefront) the tiles' places
-    for (int t = (int)threadIdx.x; t < tiles; t += 256) {
+    for (int t = (int)threadIdx.x; t < tiles; t += kListThreads) {
         int32_t n = 0;
         for (int r = 0; r < 32; ++r) {
             place[r * tiles + t] = n;
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(256) sample_list_kernel(const int32_t* __restr
         if (lane == 0 && blockIdx.x == gridDim.x - 1) tile_ptr[(int64_t)gridDim.x * tiles] = carry;
     }
     __syncthreads();
-    for (int r = wave; r < nr; r += 4) {
+    for (int r = wave; r < nr; r += kListThreads / kWave) {
         for (int32_t e = ptr[r0 + r] + lane; e < ptr[r0 + r + 1]; e += kWave) {
             const int c = cols[e], t = c / kCols;
             list[place[r * tiles + t] + e - at[r * w + t]] =
@@ -290,7 +292,7 @@ size_t sample_ws_bytes(const snack_layer* L, const BatchPlan& p, size_t* a_bytes
 snack_status sample_index(const snack_layer* L, hipStream_t s)
 {
     const int tiles = (L->K + kCols - 1) / kCols;
-    hipLaunchKernelGGL(sample_list_kernel, dim3((unsigned)blocks32(L->M)), dim3(256),
+    hipLaunchKernelGGL(sample_list_kernel, dim3((unsigned)blocks32(L->M)), dim3(kListThreads),
                        (size_t)32 * (2 * tiles + 1) * sizeof(int32_t), s, L->row_ptr, L->cols, L->M, tiles,
                        L->sample_list, L->sample_ptr);
     SNACK_HIP(hipGetLastError());
