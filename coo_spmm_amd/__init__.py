@@ -478,7 +478,11 @@ class Ckpt:
         return p, p + self.rows * -(-self.n // _BLOCK) * _BLOCK
 
     def _dev(self):
-        return (self._q if self._buf is None else self._buf).get_device()
+        """Its GPU, which has to be the current one."""
+        dev = (self._q if self._buf is None else self._buf).get_device()
+        if dev != torch._C._cuda_getDevice():
+            raise ValueError("the checkpoint must be on the current GPU")
+        return dev
 
     @property
     def q(self):
@@ -518,11 +522,12 @@ class Ckpt:
         y_fmt = _HIDDEN.get(dtype)
         if y_fmt is None:
             raise TypeError("a checkpoint is read as float32 or bfloat16")
+        dev = self._dev()
         own = self._q if self._buf is None else self._buf
         y = own.new_empty((self.rows, self.n), dtype=dtype)
         q, s = self._ptrs()
         _check(_lib.snack_ckpt_unpack(q, s, self.rows, self.n, self.fmt, y.data_ptr(), y_fmt,
-                                      _raw_stream(own.get_device())), "snack_ckpt_unpack")
+                                      _raw_stream(dev)), "snack_ckpt_unpack")
         return y
 
 

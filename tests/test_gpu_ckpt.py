@@ -216,6 +216,46 @@ def test_norm_backward(rows, n, hf):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dg)
 
 
+def test_past_two_to_the_31():
+    """Arrays of more than 2^31 values: the last rows are those of a call on them alone."""
+    import torch
+    L = lib()
+    rows, n, last = 214800, 10007, 70
+    assert rows * n > 2 ** 31 and torch.cuda.mem_get_info()[0] > 80e9
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn(rows, n, device="cuda", generator=g)
+    gain = torch.randn(n, device="cuda", generator=g)
+    tail = x[rows - last:].clone()
+    try:
+        say("large pack")
+        ck, ct = L.Ckpt.pack(x, L.INT8), L.Ckpt.pack(tail, L.INT8)
+        assert torch.equal(ck.q[rows - last:], ct.q) and torch.equal(ck.s[rows - last:], ct.s)
+        for dt in (torch.float32, torch.bfloat16):
+            say("large unpack", dt)
+            assert torch.equal(ck.unpack(dt)[rows - last:], ct.unpack(dt))
+        say("large norm")
+        h, y, rstd, cy = L.rmsnorm_fwd(x, gain, 1e-6, residual=x, q_format=L.E4M3)
+        ht, yt, rt, cyt = L.rmsnorm_fwd(tail, gain, 1e-6, residual=tail, q_format=L.E4M3)
+        for a, b in ((h, ht), (y, yt), (rstd, rt), (cy.q, cyt.q), (cy.s, cyt.s)):
+            assert torch.equal(a[rows - last:], b)
+        del h, cy
+        say("large norm backward")
+        for hid, hid_t in ((x, tail), (ck, ct)):
+            dx, dg = L.rmsnorm_bwd(hid, gain, rstd, y, dR=x)
+            dxt, _ = L.rmsnorm_bwd(hid_t, gain, rt, yt, dR=tail)
+            assert torch.equal(dx[rows - last:], dxt) and bool(torch.isfinite(dg).all())
+            del dx
+        say("large gelu")
+        assert torch.equal(L.gelu_ckpt_bwd(ck, y)[rows - last:], L.gelu_ckpt_bwd(ct, yt))
+        a, cx, ca = L.gelu_ckpt_fwd(x, L.E4M3)
+        at, cxt, cat = L.gelu_ckpt_fwd(tail, L.E4M3)
+        for u, v in ((a, at), (cx.q, cxt.q), (ca.q, cat.q), (ca.s, cat.s)):
+            assert torch.equal(u[rows - last:], v)
+    finally:
+        x = y = a = None
+        torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("rows,n", [(1, 1), (5, 33), (64, 500), (3, 4999), (130, 3100)])
 def test_gelu_checkpointed(rows, n):
     import torch
