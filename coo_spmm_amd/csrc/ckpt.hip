@@ -149,7 +149,8 @@ __device__ inline float gelu_fwd_value(float x)
 {
     const GeluTerms g = gelu_terms(x);
     const float q = g.e * g.r;
-    return x * (x < 0.0f ? q : 1.0f - q);
+    // -|x| q, and x - |x| q past 0, rounded once; |x| stays finite where x is not (0 and x at the infinities)
+    return fmaf(-g.a, q, x < 0.0f ? 0.0f : x);
 }
 // Phi(x) + x phi(x); 0 and 1 at the infinities
 __device__ inline float gelu_slope_value(float x)

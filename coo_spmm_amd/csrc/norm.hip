@@ -45,22 +45,24 @@ constexpr int64_t kStreamBytes = 256ll << 20;
 constexpr int kSumCols = 32, kSumRows = 32;      // final sum: columns and row strides of a workgroup
 
 // x added over the lanes of a wavefront, the same tree in every lane
-__device__ inline float wave_sum(float x)
+template <typename T>
+__device__ inline T wave_sum(T x)
 {
 #pragma unroll
     for (int m = kWave / 2; m >= 1; m >>= 1) x += __shfl_xor(x, m, kWave);
     return x;
 }
 
-// the same over a workgroup; part holds 16 floats.  Every thread gets the sum;
+// the same over a workgroup; part holds 16 numbers.  Every thread gets the sum;
 // safe to call again at once with the other half of a doubled buffer
-__device__ inline float group_sum(float x, float* part)
+template <typename T>
+__device__ inline T group_sum(T x, T* part)
 {
     x = wave_sum(x);
     const int w = (int)threadIdx.x / kWave, nw = (int)blockDim.x / kWave;
     if ((threadIdx.x & (kWave - 1)) == 0) part[w] = x;
     __syncthreads();
-    float s = 0.0f;
+    T s = 0;
 #pragma unroll 4
     for (int i = 0; i < nw; ++i) s += part[i];
     return s;
@@ -178,11 +180,39 @@ __device__ inline f32x4 hidden4(const FwdArgs& A, int64_t at, int left)
     return A.R ? hidden4<HF>(x, load4((const typename HType<HF>::T*)A.R + at, left)) : x;
 }
 
+// h^2 of four features added in 64 bits: squares of fp32 numbers neither round nor overflow there
+__device__ inline double add_squares(double s, f32x4 h)
+{
+    s = fma((double)h.x, (double)h.x, s);
+    s = fma((double)h.y, (double)h.y, s);
+    s = fma((double)h.z, (double)h.z, s);
+    return fma((double)h.w, (double)h.w, s);
+}
+
+// rstd as an fp32 number and what is left of it.  y = h rstd gain is then rounded once (to within a few 2^-48):
+// a value that sits next to a border of the 8-bit grid would otherwise go to the wrong side about four times as
+// often, and an error of rstd moves a whole row the same way.
+struct Rstd {
+    float hi, lo;
+};
+__device__ inline Rstd rstd_of(double ss, const FwdArgs& A)
+{
+    const double r = 1.0 / sqrt(ss / (double)A.n + (double)A.eps);
+    const float hi = (float)r;
+    return {hi, (float)(r - (double)hi)};
+}
+__device__ inline float scaled(float h, float g, Rstd r)
+{
+    const float u = h * r.hi;
+    const float e = fmaf(h, r.lo, fmaf(h, r.hi, -u));
+    return fmaf(u, g, e * g);
+}
+
 // y of four features and what is kept of it
 template <int QF>
-__device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t at, int left, f32x4 h, f32x4 g, float r)
+__device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t at, int left, f32x4 h, f32x4 g, Rstd r)
 {
-    const f32x4 y = h * r * g;
+    const f32x4 y = {scaled(h.x, g.x, r), scaled(h.y, g.y, r), scaled(h.z, g.z, r), scaled(h.w, g.w, r)};
     if (A.Y) store4(A.Y + at, y, left, A.stream);
     if constexpr (QF != SNACK_F32) {
         const int64_t blk = row * A.per_row + f / kCkptBlock;
@@ -194,7 +224,7 @@ __device__ inline void finish4(const FwdArgs& A, int64_t row, int64_t f, int64_t
 template <int HF, int QF, bool WG>
 __global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
 {
-    __shared__ float part[16];
+    __shared__ double part[16];
     using T = typename HType<HF>::T;
     const int64_t row = WG ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + threadIdx.x / kWave;
     if (row >= A.rows) return;   // never with WG
@@ -222,16 +252,16 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
         h[i] = kept4(h[i], n - 4 * (t + i * nt));
         g[i] = kept4(g[i], n - 4 * (t + i * nt));
     }
-    float ss = 0.0f;
+    double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int f = 4 * (t + i * nt);
         if (A.H) store4((T*)A.H + base + f, h[i], n - f, A.stream);
-        ss += dot4(h[i], h[i]);
+        ss = add_squares(ss, h[i]);
     }
     ss = WG ? group_sum(ss, part) : wave_sum(ss);
-    const float r = 1.0f / sqrtf(ss / (float)A.n + A.eps);
-    if (t == 0) A.rstd[row] = r;
+    const Rstd r = rstd_of(ss, A);
+    if (t == 0) A.rstd[row] = r.hi;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int f = 4 * (t + i * nt);
@@ -244,18 +274,18 @@ __global__ void __launch_bounds__(WG ? 1024 : 256) norm_fwd_kernel(FwdArgs A)
 template <int HF, int QF>
 __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(FwdArgs A)
 {
-    __shared__ float part[16];
+    __shared__ double part[16];
     using T = typename HType<HF>::T;
     const int64_t row = blockIdx.x, base = row * A.n;
-    float ss = 0.0f;
+    double ss = 0.0;
     for (int64_t f = 4 * (int64_t)threadIdx.x; f < A.n; f += 4 * kLongThreads) {
         const f32x4 h = hidden4<HF>(A, base + f, A.n - f);
         if (A.H) store4(reinterpret_cast<T*>(A.H) + base + f, h, A.n - f, A.stream);
-        ss += dot4(h, h);
+        ss = add_squares(ss, h);
     }
     ss = group_sum(ss, part);
-    const float r = 1.0f / sqrtf(ss / (float)A.n + A.eps);
-    if (threadIdx.x == 0) A.rstd[row] = r;
+    const Rstd r = rstd_of(ss, A);
+    if (threadIdx.x == 0) A.rstd[row] = r.hi;
     for (int64_t f = 4 * (int64_t)threadIdx.x; (f & ~(int64_t)(kCkptBlock - 1)) < A.n; f += 4 * kLongThreads)
         finish4<QF>(A, row, f, base + f, A.n - f, hidden4<HF>(A, base + f, A.n - f), load4(A.gain + f, A.n - f), r);
 }

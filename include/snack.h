@@ -362,7 +362,7 @@ snack_status snack_ckpt_unpack(const uint8_t* Q, const uint8_t* S, int64_t rows,
 /*
  * Root-mean-square norm with the residual's addition:
  *   h = X + R,   y = h rstd gain,   rstd = 1 / sqrt(mean over the row of h^2 + eps).
- * The sum of squares is held in fp32.
+ * The sum of squares is held in 64 bits and y rounded once.
  *   X     device float[rows, n];  gain device float[n];  eps >= 0.
  *   R, H  the residual stream before and after, device [rows, n] in h_fmt
  *         (SNACK_F32, or SNACK_BF16: the sum is rounded to it once and the norm
