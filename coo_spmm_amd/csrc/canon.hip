@@ -494,19 +494,20 @@ snack_status build_idx16(snack_layer* L, hipStream_t s)
     return SNACK_OK;
 }
 
-snack_status canon_index_tail(snack_layer* L, hipStream_t s, bool idx16_done, bool empty_cleared)
+snack_status canon_index_tail(snack_layer* L, hipStream_t s, bool idx16_done, bool empty_cleared, bool splits_done)
 {
     if (!idx16_done) SNACK_CHECK(build_idx16(L, s));
-    L->vals_t_stale = false;
-    for (int i = 0; i < kTileWidths; ++i) {
-        L->fwd.split[i].valid = false;
-        L->tr.split[i].valid = false;
+    const bool made = !stream_capturing(s);
+    L->vals_t_stale = !made;
+    for (View* v : {&L->fwd, &L->tr}) {
+        for (SplitTab& t : v->split) t.valid = made && splits_done && t.S >= 2;
+        if (v->split_used && !splits_done) SNACK_CHECK(split_index(*v, s));
     }
     SNACK_CHECK(build_view_partitions(L, s, empty_cleared));
     L->sample_valid = false;
     if (L->sample_used) {
         SNACK_CHECK(sample_index(L, s));
-        L->sample_valid = true;
+        L->sample_valid = made;
     }
     return SNACK_OK;
 }
@@ -519,7 +520,7 @@ snack_status refresh_vals_t(snack_layer* L, hipStream_t s)
                            L->nnz, L->vals_t);
         SNACK_HIP(hipGetLastError());
     }
-    L->vals_t_stale = false;
+    if (!stream_capturing(s)) L->vals_t_stale = false;
     return SNACK_OK;
 }
 

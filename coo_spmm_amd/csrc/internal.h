@@ -40,8 +40,9 @@ enum KernelClass : int {
 
 // For the slice-tiled kernels: the gathered operand's rows split into S
 // slices that each fit in LDS; tab[s * nkeys + r] is the first entry of key r
-// whose index lies in slice s or later (s = 0..S).  Rebuilt lazily after every
-// change of the index.
+// whose index lies in slice s or later (s = 0..S).  Made by the first call that
+// reads it and from then on with every change of the index, so that a call
+// captured in a graph reads the present one.
 constexpr int kTileWidths = 4;   // batch tiles 8, 16, 32, 64
 // Floats per staged row of the slice-tiled passes: a batch tile's columns,
 // padded by 16 bytes below 64 columns so that consecutive rows start in
@@ -83,6 +84,7 @@ struct View {
     int32_t* empty_keys = nullptr;  // [nkeys]: keys with no entry, ascending
     int32_t* n_empty = nullptr;     // device count of empty_keys
     SplitTab split[kTileWidths];
+    mutable bool split_used = false;   // a call has read one of them
 };
 
 struct Scratch {
@@ -120,6 +122,9 @@ struct snack_layer {
     uint64_t b16_version = 0;
     int32_t* col_ptr = nullptr;   // [K+1]
     bool vals_t_stale = true;
+    // a step of vals alone was recorded into a graph: any replay may have moved
+    // them past vals_t since it was last made
+    bool vals_in_graph = false;
     // dW in transposed order from the last backward (bit-identical to the
     // canonical dW it was produced with); lets SGD update both value copies
     float* dwt = nullptr;
@@ -192,6 +197,12 @@ struct ProfScope {
     }
 };
 
+// Whether work queued on s is recorded into a graph: then nothing is made by
+// the time the call returns, and what the recorded work reads may have changed
+// by the time it runs.  So a capturing call marks nothing as made, and records
+// the making of whatever a later call could leave out of date (layer.hip).
+bool stream_capturing(hipStream_t s);
+
 // ---- allocation helpers (layer.hip) ---------------------------------------
 snack_status layer_alloc(snack_layer* L, void** p, size_t bytes);
 
@@ -222,8 +233,10 @@ snack_status canon_sort_input(snack_layer* L, const int32_t* rows, const int32_t
 snack_status canon_build_index(snack_layer* L, hipStream_t s);
 // The part of canon_build_index after row_ptr and the transposed view exist
 // (for callers that build those themselves): partitions of both views, flags,
-// and the 16-bit index copies unless the caller wrote them (idx16_done).
-snack_status canon_index_tail(snack_layer* L, hipStream_t s, bool idx16_done = false, bool empty_cleared = false);
+// and the 16-bit index copies and slice tables unless the caller wrote them
+// (idx16_done, splits_done: all those allocated).
+snack_status canon_index_tail(snack_layer* L, hipStream_t s, bool idx16_done = false, bool empty_cleared = false,
+                              bool splits_done = false);
 // vals_t[iperm[k]] = vals[k]
 snack_status refresh_vals_t(snack_layer* L, hipStream_t s);
 // the views' 16-bit index copies from their 32-bit indices (where allocated)
@@ -329,6 +342,7 @@ snack_status spmm_backward_fused(const snack_layer* L, const float* xt, const fl
 // need for a batch plan
 int tile_splits(const snack_layer* L, const View& v, int btile);
 snack_status alloc_split_tables(snack_layer* L);
+snack_status split_index(const View& v, hipStream_t s);   // the invalid tables of v, from the present index
 size_t tile_part_bytes(const snack_layer* L, const BatchPlan& p);
 // several 64-column batch tiles: dX and dW in one slice-tiled column pass (one dW slab per tile,
 // added up in tile order into dW_t, then permuted into canonical order into dW)

@@ -1748,12 +1748,7 @@ snack_status rebuild(snack_layer* L, const PruneScratch& ps, hipStream_t s, cons
                            ps.old_bm, ps.kept_bm, words, M, K, nbi, nbj, ps.cvcnt, ps.cvtot, ps.cvband, ps.rcnt,
                            ps.rtot, ps.rband, ps.ocnt, ps.otot, ps.oband, ps.vcopy, o, tabs);
         SNACK_HIP(hipGetLastError());
-        SNACK_CHECK(canon_index_tail(L, s, /*idx16_done=*/true, /*empty_cleared=*/true));
-        for (int w = 0; w < kTileWidths; ++w) {
-            if (tabs.rtab[w]) L->fwd.split[w].valid = true;
-            if (tabs.ctab[w]) L->tr.split[w].valid = true;
-        }
-        return SNACK_OK;
+        return canon_index_tail(L, s, /*idx16_done=*/true, /*empty_cleared=*/true, /*splits_done=*/true);
     }
     // ---- a layer too sparse for the tiles: the canonical arrays from the bitmap in unit order,
     // then the index build ----

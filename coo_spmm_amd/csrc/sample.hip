@@ -304,10 +304,7 @@ snack_status sample_dw(const snack_layer* L, const void* a, const void* x, int B
     ProfScope prof(KC_SDDMM_DW, s);
     if (!L->sample_valid) {
         SNACK_CHECK(sample_index(L, s));
-        // a list recorded into a graph is only made when the graph runs: eager calls make their own
-        hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-        SNACK_HIP(hipStreamIsCapturing(s, &cap));
-        L->sample_valid = cap == hipStreamCaptureStatusNone;
+        L->sample_valid = !stream_capturing(s);
         L->sample_used = true;
     }
     SampleArgs t;

@@ -2328,11 +2328,19 @@ snack_status launch_stream_bwd(const BatchPlan& p, const snack_layer* L, const f
     return SNACK_OK;
 }
 
-// the split table of width index w of view v, valid: when it is stale, every
-// stale table of the view is rebuilt in one pass over its index
+// the split table of width index w of view v, valid for what is queued on s after it
 snack_status ensure_split(const View& v, int w, hipStream_t s)
 {
-    if (v.split[w].S < 2 || v.split[w].valid) return SNACK_OK;
+    if (v.split[w].S < 2) return SNACK_OK;
+    v.split_used = true;
+    return v.split[w].valid ? SNACK_OK : split_index(v, s);
+}
+
+}  // namespace
+
+// every invalid table of the view in one pass over its index
+snack_status split_index(const View& v, hipStream_t s)
+{
     TabSet ts;
     ts.inv_nidx = 1.0 / (double)v.nidx;
     for (int i = 0; i < kTileWidths; ++i) {
@@ -2344,10 +2352,13 @@ snack_status ensure_split(const View& v, int w, hipStream_t s)
     hipLaunchKernelGGL(split_tables_kernel, dim3((unsigned)((v.nkeys + 3) / 4)), dim3(256), 0, s, v.ptr, v.idx,
                        v.nkeys, v.nidx, ts);
     SNACK_HIP(hipGetLastError());
+    const bool made = !stream_capturing(s);
     for (int i = 0; i < kTileWidths; ++i)
-        if (ts.tab[i]) v.split[i].valid = true;
+        if (ts.tab[i]) v.split[i].valid = made;
     return SNACK_OK;
 }
+
+namespace {
 
 inline int tile_index(int btile)
 {

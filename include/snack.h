@@ -162,6 +162,10 @@ snack_status snack_forward_chain(snack_layer* const* layers, int32_t n, const in
  *   dW  device float[nnz] in canonical slot order, 16-byte aligned, or NULL;
  *       overwritten (the caller accumulates if it wants to).  Stored zeros get
  *       a gradient.
+ * A call captured in a HIP graph takes the layer as it is at each replay, its values
+ * and its positions (SGD steps and drop/regrow between the replays count; dX's column-ordered
+ * copy of the values is remade in every replay).  The graph holds the workspace's address, so
+ * it is captured again after a snack_layer_reserve that grew the workspace.
  */
 snack_status snack_backward(snack_layer* layer, const float* X, const float* dY,
                             float* dX, float* dW, int32_t B, snack_stream stream);
@@ -174,7 +178,9 @@ snack_status snack_backward(snack_layer* layer, const float* X, const float* dY,
  * snack_sgd_step(layer, dW, lr).  X, dY, dW are required (dW written as by
  * snack_backward; NULL only for a layer with no entries); dX may be NULL.  Where the column pass computes dW, it also
  * steps the layer's column-ordered value copy in place, so the step moves one
- * copy's worth of bytes less than the two separate calls.
+ * copy's worth of bytes less than the two separate calls.  Captured in a HIP graph
+ * it steps both copies in every replay; it is captured again after any other
+ * change of the values.
  */
 snack_status snack_backward_sgd(snack_layer* layer, const float* X, const float* dY, float* dX, float* dW,
                                 float lr, int32_t B, snack_stream stream);
@@ -412,8 +418,7 @@ snack_status snack_gelu_ckpt_bwd(const uint8_t* QX, const uint8_t* SX, const flo
  * as there; sums in fp32.  A NaN or an infinity reaches the dW of its own row of
  * W (from dY) or its own column (from x) only, where it gives a NaN or an
  * infinity.  dY below 2^-109 in magnitude may lose its last bits in dW.
- * A call captured in a graph is captured again after a drop/regrow; its dW, but
- * not its dX, is right without that.
+ * Captured in a HIP graph as snack_backward is.
  */
 snack_status snack_backward_ckpt(snack_layer* layer, const uint8_t* Q, const uint8_t* S, int32_t fmt, const float* dY,
                                  float* dX, float* dW, int32_t B, snack_stream stream);
