@@ -186,10 +186,15 @@ snack_status wide_sddmm(const snack_layer* L, const float* xt, const float* dyt,
         hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(kWideThreads), 0, s, L->rows, L->cols, L->nnz, xt, dyt,
                            p.bp, dW);
     };
-    // the bits are the same.  Measured (us, a call for dW with one entry a wavefront : with four): 8000 entries, 2048 rows
-    // 27.0 : 31.4; 23592 entries 1000 rows 27.0 : 26.9; 40000, 256 rows 16.8 : 13.4, 2048 rows 61.6 : 60.9;
-    // 150000, 100 rows 40.7 : 23.5, 1000 rows 95.7 : 87.9
-    if (L->nnz >= 32768) go(wide_sddmm_kernel<4>, 4);
+    // The bits are the same.  Four entries a wavefront save launches of wavefronts in narrow batches and reads of dyt
+    // where rows are long enough to be shared; in wide batches over short rows neither counts, and a group that
+    // crosses a row runs its entries one after the other.  Measured (us, a call for dW, one : four), 3000 columns:
+    //   8000 entries,  2048 batch rows 27.0 : 31.4;  23592 entries, 1000 batch rows 27.0 : 26.9
+    //   100000 entries, 1 a row:  256 batch rows 61 : 55, 384 92 : 89, 768 177 : 185, 2048 504 : 540
+    //                   2 a row:  384 batch rows 66 : 60, 512 76 : 76, 768 115 : 126, 2048 317 : 374
+    //                   4 a row:  512 batch rows 56 : 52, 768 82 : 89;    8 a row: 768 65 : 63, 1024 87 : 91
+    //                  16 a row: 1024 batch rows 115 : 112, 2048 218 : 221;  30 a row: 2048 189 : 183
+    if (L->nnz >= 32768 && p.bp <= 384 + 56 * (L->nnz / L->M)) go(wide_sddmm_kernel<4>, 4);
     else go(wide_sddmm_kernel<1>, 1);
     SNACK_HIP(hipGetLastError());
     return SNACK_OK;
