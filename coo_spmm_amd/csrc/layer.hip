@@ -59,13 +59,14 @@ void free_layer(snack_layer* L)
 
 inline hipStream_t as_stream(snack_stream s) { return reinterpret_cast<hipStream_t>(s); }
 
-size_t ws_need(const snack_layer* L, const BatchPlan& p)
+// what a call of plan p takes; sample: a dW from a checkpoint by tiles
+size_t ws_need(const snack_layer* L, const BatchPlan& p, bool sample)
 {
     const size_t a = (((size_t)L->K * p.bp * 4) + 255) & ~(size_t)255;
     const size_t b = (((size_t)L->M * p.bp * 4) + 255) & ~(size_t)255;
-    // the operands of the dW from a checkpoint are used up before a pass writes partial sums in their place
-    const size_t part = tile_part_bytes(L, p) + wide_dw_bytes(L, p), sample = sample_ws_bytes(L, p);
-    return a + b + (part > sample ? part : sample);
+    // the operands of the tiles are used up before a pass writes partial sums in their place
+    const size_t part = tile_part_bytes(L, p) + wide_dw_bytes(L, p), ops = sample ? sample_ws_bytes(L, p) : 0;
+    return a + b + (part > ops ? part : ops);
 }
 
 // grow the workspace to hold plan p (never shrinks); the new buffer is
@@ -73,7 +74,7 @@ size_t ws_need(const snack_layer* L, const BatchPlan& p)
 // reserve
 snack_status ensure_ws(snack_layer* L, const BatchPlan& p)
 {
-    const size_t need = ws_need(L, p);
+    const size_t need = ws_need(L, p, true);
     if (need <= L->ws_bytes) return SNACK_OK;
     void* p2 = nullptr;
     if (hipMalloc(&p2, need) != hipSuccess) {
@@ -99,9 +100,9 @@ snack_status ensure_ws(snack_layer* L, const BatchPlan& p)
 
 // the compute entry points never allocate: a batch plan whose workspace is not
 // reserved is refused before anything is launched
-snack_status ws_check(const snack_layer* L, const BatchPlan& p)
+snack_status ws_check(const snack_layer* L, const BatchPlan& p, bool sample = false)
 {
-    return ws_need(L, p) <= L->ws_bytes ? SNACK_OK : SNACK_ERR_WORKSPACE;
+    return ws_need(L, p, sample) <= L->ws_bytes ? SNACK_OK : SNACK_ERR_WORKSPACE;
 }
 
 // the largest workspace of any batch plan up to max_batch (the slice-tiled
@@ -114,7 +115,7 @@ snack_status reserve_ws(snack_layer* L, int32_t max_batch)
     size_t need = 0;
     for (int32_t b = 1;;) {
         const BatchPlan p = plan_batch(b);
-        const size_t n = ws_need(L, p);
+        const size_t n = ws_need(L, p, true);
         if (n > need) {
             need = n;
             best = p;
@@ -435,10 +436,11 @@ extern "C" snack_status snack_backward_ckpt(snack_layer* L, const uint8_t* Q, co
     hipStream_t s = as_stream(stream);
     if (!dW) return backward_impl(L, nullptr, dY, dX, nullptr, B, s, nullptr);
     const BatchPlan p = plan_batch(B);
-    SNACK_CHECK(ws_check(L, p));
+    const bool sample = sample_applies(L, p, dX != nullptr);
+    SNACK_CHECK(ws_check(L, p, sample));
     // the copies in the workspace, where this plan's passes read them
     const bool copies = p.bp > 1 && !spmm_batch_major(L, p, false, dX != nullptr, true);
-    if (sample_applies(L, p, dX != nullptr)) {
+    if (sample) {
         const bool dx_copies = dX && p.bp > 1 && !spmm_batch_major(L, p, false, true, false);
         size_t a_bytes = 0;
         (void)sample_ws_bytes(L, p, &a_bytes);

@@ -88,7 +88,8 @@ snack_status snack_layer_destroy(snack_layer* layer);
 
 /*
  * Size the per-batch workspace (feature-major copies of X and dY, and the
- * partial sums of the batch-tiled passes) for every batch up to max_batch
+ * partial sums of the batch-tiled passes or the operands of a dW from a
+ * checkpoint, whichever are more) for every batch up to max_batch
  * (1 <= max_batch <= 2^20, else SNACK_ERR_INVALID_ARG / SNACK_ERR_UNSUPPORTED).
  * The workspace never shrinks: a max_batch below the current reserve changes
  * nothing.  Growing it allocates the new workspace, synchronises the device
