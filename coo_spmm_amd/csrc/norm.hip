@@ -43,6 +43,10 @@ constexpr int kColThreads = 256;                 // column pass of rows past kRo
 // 229 MB, 107 : 113 and 4096 x 2000, 57 MB, 26.0 : 28.2.
 constexpr int64_t kStreamBytes = 256ll << 20;
 constexpr int kSumCols = 32, kSumRows = 32;      // final sum: columns and row strides of a workgroup
+// Threads of a launch at most (HIP takes fewer than 2^32 of them) and its blocks in y: what needs more, from 2^21
+// rows of a workgroup each on, is launched in pieces.
+constexpr int64_t kLaunchThreads = 1ll << 31;
+constexpr int64_t kLaunchY = 1 << 15;
 
 // x added over the lanes of a wavefront, the same tree in every lane
 template <typename T>
@@ -303,6 +307,7 @@ struct BwdArgs {
     int64_t rows, n, per_row;
     float* dgain;         // written here by the workgroups past `groups`, or null
     int groups;           // workgroups that take rows
+    int64_t col0;         // first column of this launch (norm_bwd_cols_kernel)
 };
 
 // Four features of one row of h, from feature f, in the same two steps: h and hs are the row's (its codes and
@@ -350,7 +355,7 @@ __device__ inline f32x4 hidden_row4(const void* __restrict__ h, const uint8_t* _
     }
 }
 template <int HF>
-__device__ inline const void* kept_row(const BwdArgs& A, int64_t row)
+__host__ __device__ inline const void* kept_row(const BwdArgs& A, int64_t row)
 {
     if constexpr (HF == SNACK_INT8 || HF == SNACK_E4M3) return (const uint8_t*)A.H + row * A.per_row * kCkptBlock;
     else return (const typename HType<HF>::T*)A.H + row * A.n;
@@ -507,11 +512,11 @@ __global__ void __launch_bounds__(kLongThreads) norm_bwd_mean_kernel(BwdArgs A)
     if (threadIdx.x == 0) A.mean[row] = dot / (float)A.n;
 }
 
-// second pass: a workgroup takes 1024 columns (blockIdx.y) of rows blockIdx.x, + gridDim.x, ...
+// second pass: a workgroup takes 1024 columns (col0 and blockIdx.y) of rows blockIdx.x, + gridDim.x, ...
 template <int HF>
 __global__ void __launch_bounds__(kColThreads) norm_bwd_cols_kernel(BwdArgs A)
 {
-    const int64_t at0 = 4 * ((int64_t)blockIdx.y * kColThreads + threadIdx.x);
+    const int64_t at0 = A.col0 + 4 * ((int64_t)blockIdx.y * kColThreads + threadIdx.x);
     if (at0 >= A.n) return;
     const int f = (int)at0, left = (int)(A.n - at0);
     const f32x4 g = load4(A.gain + f, left);
@@ -529,13 +534,13 @@ __global__ void __launch_bounds__(kColThreads) norm_bwd_cols_kernel(BwdArgs A)
     if (A.part) store4(A.part + (int64_t)blockIdx.x * A.n + f, acc, left);
 }
 
-// out[c] = sum of part[g][c]: 32 strided runs of rows, then the runs in order
+// out[c] = sum of part[g][c], from column c0 on: 32 strided runs of rows, then the runs in order
 __global__ void __launch_bounds__(kSumCols * kSumRows) part_sum_kernel(const float* __restrict__ part, int groups,
-                                                                       int64_t n, float* __restrict__ out)
+                                                                       int64_t n, int64_t c0, float* __restrict__ out)
 {
     __shared__ float sh[kSumRows][kSumCols + 1];
     const int tx = (int)threadIdx.x % kSumCols, ty = (int)threadIdx.x / kSumCols;
-    const int64_t c = (int64_t)blockIdx.x * kSumCols + tx;
+    const int64_t c = c0 + (int64_t)blockIdx.x * kSumCols + tx;
     float a = 0.0f;
     if (c < n) {
 #pragma unroll 8
@@ -582,15 +587,40 @@ bool gain_beside(int64_t rows, int64_t n) { return rows > 0 && rows <= 1024 && !
 bool bad_size(int64_t rows, int64_t n) { return n >= (1ll << 31) - kCkptBlock || rows >= (1ll << 31); }
 inline bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-template <int HF, int QF>
-void launch_fwd(const FwdArgs& A, hipStream_t s)
+// a pointer moved by so many elements; null stays null
+template <typename T>
+T* moved(T* p, int64_t by) { return p ? p + by : nullptr; }
+
+// the call's rows from r0 on, at most `rows` of them
+template <int HF>
+FwdArgs rows_from(FwdArgs A, int64_t r0, int64_t rows)
 {
-    if (long_rows(A.n))
-        hipLaunchKernelGGL((norm_fwd_long_kernel<HF, QF>), dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
-    else if (A.n <= kWaveRow)
-        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, false>), dim3((unsigned)((A.rows + 3) / 4)), dim3(256), 0, s, A);
-    else
-        hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, true>), dim3((unsigned)A.rows), dim3(row_threads(A.n)), 0, s, A);
+    using T = typename HType<HF>::T;
+    A.X += r0 * A.n;
+    A.R = moved((const T*)A.R, r0 * A.n);
+    A.H = moved((T*)A.H, r0 * A.n);
+    A.Y = moved(A.Y, r0 * A.n);
+    A.rstd += r0;
+    A.Q = moved(A.Q, r0 * A.per_row * kCkptBlock);
+    A.S = moved(A.S, r0 * A.per_row);
+    A.rows = A.rows - r0 < rows ? A.rows - r0 : rows;
+    return A;
+}
+
+template <int HF, int QF>
+void launch_fwd(const FwdArgs& all, hipStream_t s)
+{
+    const int threads = long_rows(all.n) ? kLongThreads : all.n <= kWaveRow ? kWave : row_threads(all.n);   // a row
+    const int64_t most = kLaunchThreads / threads;
+    for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
+        const FwdArgs A = rows_from<HF>(all, r0, most);
+        if (long_rows(A.n))
+            hipLaunchKernelGGL((norm_fwd_long_kernel<HF, QF>), dim3((unsigned)A.rows), dim3(threads), 0, s, A);
+        else if (A.n <= kWaveRow)
+            hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, false>), dim3((unsigned)((A.rows + 3) / 4)), dim3(256), 0, s, A);
+        else
+            hipLaunchKernelGGL((norm_fwd_kernel<HF, QF, true>), dim3((unsigned)A.rows), dim3(threads), 0, s, A);
+    }
 }
 template <int HF>
 void launch_fwd(const FwdArgs& A, int q_fmt, hipStream_t s)
@@ -605,9 +635,24 @@ void launch_bwd(const BwdArgs& A, hipStream_t s)
 {
     const unsigned grid = (unsigned)A.groups + (A.dgain ? (unsigned)((A.n + 4 * kGainLanes - 1) / (4 * kGainLanes)) : 0u);
     if (long_rows(A.n)) {
-        hipLaunchKernelGGL(norm_bwd_mean_kernel<HF>, dim3((unsigned)A.rows), dim3(kLongThreads), 0, s, A);
-        const unsigned cols = (unsigned)((A.n + 4 * kColThreads - 1) / (4 * kColThreads));
-        hipLaunchKernelGGL(norm_bwd_cols_kernel<HF>, dim3((unsigned)A.groups, cols), dim3(kColThreads), 0, s, A);
+        constexpr int64_t most = kLaunchThreads / kLongThreads;
+        for (int64_t r0 = 0; r0 < A.rows; r0 += most) {
+            BwdArgs P = A;
+            P.H = kept_row<HF>(A, r0);
+            P.HS = moved(A.HS, r0 * A.per_row);
+            P.rstd += r0;
+            P.dY += r0 * A.n;
+            P.mean += r0;
+            const int64_t rows = A.rows - r0 < most ? A.rows - r0 : most;
+            hipLaunchKernelGGL(norm_bwd_mean_kernel<HF>, dim3((unsigned)rows), dim3(kLongThreads), 0, s, P);
+        }
+        const int64_t cols = (A.n + 4 * kColThreads - 1) / (4 * kColThreads);
+        for (int64_t c = 0; c < cols; c += kLaunchY) {
+            BwdArgs P = A;
+            P.col0 = c * 4 * kColThreads;
+            const unsigned y = (unsigned)(cols - c < kLaunchY ? cols - c : kLaunchY);
+            hipLaunchKernelGGL(norm_bwd_cols_kernel<HF>, dim3((unsigned)A.groups, y), dim3(kColThreads), 0, s, P);
+        }
     } else if (A.n <= kWaveRow) {
         hipLaunchKernelGGL((norm_bwd_kernel<HF, 256>), dim3(grid), dim3(256), 0, s, A);
     } else {
@@ -684,7 +729,7 @@ extern "C" snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int3
     float* part = (float*)work + (long_rows(n) ? rows : 0);
     if (rows > 0) {
         const BwdArgs A{H, HS, gain, rstd, dY, dR, dX, dgain && !beside ? part : nullptr, mean, rows, n,
-                        (n + kCkptBlock - 1) / kCkptBlock, beside ? dgain : nullptr, groups};
+                        (n + kCkptBlock - 1) / kCkptBlock, beside ? dgain : nullptr, groups, 0};
         switch (h_fmt) {
         case SNACK_F32: launch_bwd<SNACK_F32>(A, s); break;
         case SNACK_BF16: launch_bwd<SNACK_BF16>(A, s); break;
@@ -695,8 +740,12 @@ extern "C" snack_status snack_rmsnorm_bwd(const void* H, const uint8_t* HS, int3
     }
     if (dgain && !beside) {
         // no rows: no partial rows, and the sum over none of them is 0
-        hipLaunchKernelGGL(part_sum_kernel, dim3((unsigned)((n + kSumCols - 1) / kSumCols)),
-                           dim3(kSumCols * kSumRows), 0, s, part, groups, n, dgain);
+        constexpr int64_t most = kLaunchThreads / kSumRows;   // columns
+        for (int64_t c0 = 0; c0 < n; c0 += most) {
+            const int64_t cols = n - c0 < most ? n - c0 : most;
+            hipLaunchKernelGGL(part_sum_kernel, dim3((unsigned)((cols + kSumCols - 1) / kSumCols)),
+                               dim3(kSumCols * kSumRows), 0, s, part, groups, n, c0, dgain);
+        }
         SNACK_HIP(hipGetLastError());
     }
     return SNACK_OK;

@@ -60,3 +60,64 @@ def test_plain_calls_need_no_room_for_tiles():
         assert_close("dW", host(dW3), *oracle.backward_dw(M, K, r, c, xv, dY))
     finally:
         layer.close()
+
+
+@pytest.mark.parametrize("rows,n,last", [((1 << 22) + 70, 3, 100), ((1 << 26) + 5, 4, 100)])
+def test_norm_of_more_rows_than_a_launch_takes(rows, n, last):
+    """From 2^22 rows of a workgroup each (2^26 of a wavefront) on a launch would pass 2^32 threads: the last rows, and
+    those on both sides of the pieces' border, are those of a call on them alone."""
+    import torch
+    L = lib()
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x, dr = (torch.randn(rows, n, device="cuda", generator=g) for _ in range(2))
+    gain = torch.randn(n, device="cuda", generator=g)
+    res = torch.randn(rows, n, device="cuda", generator=g).bfloat16()
+    say("many rows", rows, n)
+    h, y, rstd, ck = L.rmsnorm_fwd(x, gain, 1e-6, residual=res, q_format=L.E4M3)
+    edge = 1 << 21 if n == 3 else 1 << 25
+    pieces = [slice(rows - last, rows), slice(edge - 30, edge + 30)]
+    kept = []
+    for p in pieces:
+        h2, y2, r2, c2 = L.rmsnorm_fwd(x[p], gain, 1e-6, residual=res[p], q_format=L.E4M3)
+        for a, b in ((h, h2), (y, y2), (rstd, r2), (ck.q, c2.q), (ck.s, c2.s)):
+            assert torch.equal(a[p], b)
+        kept.append(c2)
+    for hid, parts in ((h, [h[p] for p in pieces]), (ck, kept)):
+        say("many rows backward", rows, n)
+        dx, dg = L.rmsnorm_bwd(hid, gain, rstd, y, dR=dr)
+        for p, part in zip(pieces, parts):
+            assert torch.equal(dx[p], L.rmsnorm_bwd(part, gain, rstd[p], y[p], dR=dr[p])[0])
+        if hid is h:
+            # a group adds up its rows' terms in turn, then 8 partial rows a run and 31 runs; 2 roundings of a term
+            terms = y.double() * (h.double() * rstd.double()[:, None])
+            groups = 256 if n == 3 else 4096     # the sums that are added up in turn: of workgroups, of wavefronts
+            tol = (rows // groups + 50) * O.U32 * terms.abs().sum(0)
+            assert ((dg.double() - terms.sum(0)).abs() <= tol).all()
+
+
+def test_norm_of_a_row_longer_than_a_launch():
+    """2^27 features: the sum of dgain and the columns of dX in several launches."""
+    import torch
+    L = lib()
+    rows, n, eps = 2, (1 << 27) + 77, 1e-6
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x, dy = (torch.randn(rows, n, device="cuda", generator=g) for _ in range(2))
+    gain = torch.randn(n, device="cuda", generator=g)
+    say("long row")
+    _, y, rstd, _ = L.rmsnorm_fwd(x, gain, eps)
+    xd, gd, dd = x.double(), gain.double(), dy.double()
+    rd = ((xd * xd).mean(-1) + float(np.float32(eps))).rsqrt()
+    assert ((rstd.double() - rd).abs() <= 1.01 * O.U32 * rd).all()
+    want = xd * rd[:, None] * gd
+    assert ((y.double() - want).abs() <= 1.01 * O.U32 * want.abs() + 2.0 ** -149).all()
+    del want, y
+    say("long row backward")
+    dx, dg = L.rmsnorm_bwd(x, gain, rstd, dy)
+    xh, w = xd * rstd.double()[:, None], dd * gd
+    m = (w * xh).mean(-1, keepdim=True)
+    # the mean: a thread adds up n / 4096 groups of four in turn, then 6 levels, 16 wavefronts and 6 of a term
+    tol = rstd.double()[:, None] * (6 * O.U32 * (w.abs() + (xh * m).abs())
+                                    + (n // 4096 + 32) * O.U32 * xh.abs() * (w * xh).abs().mean(-1, keepdim=True))
+    assert ((dx.double() - rstd.double()[:, None] * (w - xh * m)).abs() <= tol).all()
+    terms = dd * xh
+    assert ((dg.double() - terms.sum(0)).abs() <= 4 * O.U32 * terms.abs().sum(0)).all()
