@@ -25,6 +25,8 @@
 // 10000 x 1500 from an int8 checkpoint, 195 MB in 40 us with both.
 #include "ckpt.h"
 
+#include <float.h>
+
 namespace snack {
 namespace {
 
@@ -209,7 +211,8 @@ __device__ inline float scaled(float h, float g, Rstd r)
 {
     const float u = h * r.hi;
     const float e = fmaf(h, r.lo, fmaf(h, r.hi, -u));
-    return fmaf(u, g, e * g);
+    const float y = fmaf(u, g, e * g);
+    return fabsf(y) <= FLT_MAX ? y : u * g;   // an infinite gain: e g may be a NaN or the other infinity
 }
 
 // y of four features and what is kept of it
