@@ -121,3 +121,81 @@ def test_norm_of_a_row_longer_than_a_launch():
     assert ((dx.double() - rstd.double()[:, None] * (w - xh * m)).abs() <= tol).all()
     terms = dd * xh
     assert ((dg.double() - terms.sum(0)).abs() <= 4 * O.U32 * terms.abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("hf", ["f32", "bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("rows,n", [(20000, 96), (9000, 700), (3333, 1100), (1500, 4999), (700, 9000), (600, 15001),
+                                    (1000, 17001), (3000, 3)])
+def test_norm_backward_several_rows_a_workgroup(rows, n, hf):
+    """dgain from partial rows of several rows each, in every kernel of the gradient."""
+    import torch
+    L = lib()
+    key = f"sizes/normb/{rows}x{n}"
+    x, dy, dr = (normal((rows, n), key + k) for k in ("/h", "/dy", "/dr"))
+    gain = (1 + 0.1 * normal((n,), key + "/g")).astype(np.float32)
+    rstd = (1 / np.sqrt((x.astype(np.float64) ** 2).mean(-1) + 1e-6)).astype(np.float32)
+    if hf in ("int8", "e4m3"):
+        h = L.Ckpt.pack(dev(x), O.INT8 if hf == "int8" else O.E4M3)
+        hv = host(h.unpack()).astype(np.float64)
+    else:
+        h = dev(x, torch.bfloat16 if hf == "bf16" else None)
+        hv = h.double().cpu().numpy()
+    say("several rows", rows, n, hf)
+    dx, dg = L.rmsnorm_bwd(h, dev(gain), dev(rstd), dev(dy), dev(dr))
+    dxr, dgr, ax, ag = O.norm_bwd(hv, gain, rstd, dy, dr)
+    # the mean: at most 20 features a thread, 6 levels, 16 wavefronts, 3 of a term; 6 more to dx
+    assert (np.abs(host(dx) - dxr) <= 51 * O.U32 * ax).all()
+    # a unit's rows in turn (256 units at least), 3 wavefronts, 1024 / 32 partial rows in turn, 31 runs, 2 of a term
+    tol = (-(-rows // 256) + 3 + 32 + 31 + 2) * O.U32 * ag
+    assert (np.abs(host(dg) - dgr) <= tol).all()
+
+
+def test_norm_dgain_of_many_rows():
+    """Over a thousand rows a workgroup, against the column sums in 64 bits."""
+    import torch
+    L = lib()
+    rows, n = 400000, 1500
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x, dy = (torch.randn(rows, n, device="cuda", generator=g) for _ in range(2))
+    gain, rstd = torch.randn(n, device="cuda", generator=g), torch.rand(rows, device="cuda", generator=g) + 0.5
+    ck = L.Ckpt.pack(x, L.INT8)
+    for h, hv in ((x, x), (ck, ck.unpack())):
+        say("many rows dgain")
+        _, dg = L.rmsnorm_bwd(h, gain, rstd, dy)
+        want, mag = torch.zeros(n, device="cuda", dtype=torch.float64), torch.zeros(n, device="cuda", dtype=torch.float64)
+        for a in range(0, rows, 50000):
+            t = dy[a:a + 50000].double() * (hv[a:a + 50000].double() * rstd[a:a + 50000].double()[:, None])
+            want += t.sum(0)
+            mag += t.abs().sum(0)
+        assert ((dg.double() - want).abs() <= (-(-rows // 256) + 68) * O.U32 * mag).all()
+
+
+@pytest.mark.parametrize("M,K,nnz", [(2000, 2000, 200000), (1050, 3200, 168000), (1050, 3200, 60000)])
+def test_layer_gradients_two_wavefronts_a_tile(M, K, nnz):
+    """Layers of 1008 and of 825 tiles: two tiles a workgroup, and an odd one left; batches below a step a wavefront."""
+    from tests.test_gpu_ckpt import _layer_case
+    _layer_case(M, K, nnz, (8, 16, 33, 100), f"sizes/two/{M}x{K}/{nnz}", [O.INT8])
+
+
+@pytest.mark.parametrize("power", [-109, -118, -126])
+def test_layer_dw_of_tiny_gradients(power):
+    """dY's three parts are exact from 2^-109 on; below that the last ends at steps of 2^-133, so a term may lose less
+    than that times its x."""
+    L = lib()
+    M, K, nnz, B, key = 300, 260, 12000, 64, "sizes/tiny"
+    rows, cols, vals = random_layer(M, K, nnz, key)
+    layer = L.SnackLayer(M, K, dev(rows), dev(cols), dev(vals))
+    try:
+        dY = normal((B, M), key + "/dy")
+        dY = (np.sign(dY) * (1 + np.abs(dY) % 1) * 2.0 ** power).astype(np.float32)
+        ck = L.Ckpt.pack(dev(normal((B, K), key + "/x") * 4096), O.INT8)
+        say("tiny", power)
+        _, dW = layer.backward_ckpt(ck, dev(dY), want_dx=False)
+        r, c, _ = (host(t) for t in layer.export())
+        xv, d = host(ck.unpack()).astype(np.float64), dY.astype(np.float64)
+        want, mag = (d[:, r] * xv[:, c]).sum(0), (np.abs(d[:, r]) * np.abs(xv[:, c])).sum(0)
+        # 3 B additions in fp32 and the steps in which they end
+        tol = 3 * B * (O.U32 * mag + 2.0 ** -150) + (0 if power >= -109 else 2.0 ** -133 * np.abs(xv[:, c]).sum(0))
+        assert (np.abs(host(dW) - want) <= tol).all(), np.abs(host(dW) - want).max() / mag.max()
+    finally:
+        layer.close()
