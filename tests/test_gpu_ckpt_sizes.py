@@ -199,3 +199,29 @@ def test_layer_dw_of_tiny_gradients(power):
         assert (np.abs(host(dW) - want) <= tol).all(), np.abs(host(dW) - want).max() / mag.max()
     finally:
         layer.close()
+
+
+def test_layer_dw_operands_past_two_gb():
+    """The tiles' operands lie at 32-bit offsets of a scalar base: dY's take 2.4 GB here."""
+    import torch
+    L = lib()
+    M, K, B, key = 10000, 1000, 40000, "sizes/operands"
+    nnz = M * K // 32
+    rows, cols, vals = random_layer(M, K, nnz, key)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    X, dY = torch.randn(B, K, device="cuda", generator=g), torch.randn(B, M, device="cuda", generator=g)
+    layer = L.SnackLayer(M, K, dev(rows), dev(cols), dev(vals), max_batch=B)
+    try:
+        ck = L.Ckpt.pack(X, L.E4M3)
+        say("operands", M, K, B)
+        _, dW = layer.backward_ckpt(ck, dY, want_dx=False)
+        r, c, _ = layer.export()
+        xv = ck.unpack()
+        for i in (0, nnz // 2, nnz - 1500):
+            k = slice(i, i + 1500)
+            a, b = dY[:, r[k].long()].double(), xv[:, c[k].long()].double()
+            tol = 3 * B * O.U32 * (a.abs() * b.abs()).sum(0)
+            assert ((dW[k].double() - (a * b).sum(0)).abs() <= tol).all()
+    finally:
+        layer.close()
+        torch.cuda.empty_cache()
