@@ -81,6 +81,8 @@ def main():
     ap.add_argument("--steps", type=int, default=200)
     ap.add_argument("--lr", type=float, default=20.0)
     a = ap.parse_args()
+    if a.steps < 1:
+        ap.error("--steps must be at least 1")
     block = CheckpointedBlock(a.width, a.hidden, a.sparsity, a.rows, L.INT8 if a.format == "int8" else L.E4M3)
     gen = torch.Generator(device="cuda").manual_seed(1)
     residual = torch.randn(a.rows, a.width, device="cuda", generator=gen).bfloat16()
