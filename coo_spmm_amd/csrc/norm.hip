@@ -22,7 +22,9 @@
 // Measured (a copy of 1 GiB runs at 5.2 TB/s): forward 8192 x 5000, bf16 residual,
 // e4m3 checkpoint, 534 MB in 109 us (4.9 TB/s); 1 x 768 in 2.7 us (a launch).
 // Gradient 3333 x 4999, fp32 h, 266 MB in 44 us and 4.9 us for the partial rows;
-// 10000 x 1500 from an int8 checkpoint, 195 MB in 40 us with both.
+// 10000 x 1500 from an int8 checkpoint, 195 MB in 40 us with both.  Rows read twice: 2000 x 20000, bf16 residual, int8
+// checkpoint, 520 MB in 127 us, gradient from bf16 h 128 us; 200000 x 3, a workgroup a row of three values, 1.2 and
+// 0.9 ms.
 #include "ckpt.h"
 
 #include <float.h>
@@ -582,9 +584,10 @@ int bwd_groups(int64_t rows, int64_t n)
 }
 
 // Whether dgain is summed beside the rows in the same launch, which reads dY and h twice and walks all rows in every
-// workgroup, instead of from partial rows.  Measured (us on the GPU, partial rows : beside, int8 h): 256 x 768 6.2 : 3.5,
-// 1024 x 768 7.2 : 8.2 (13.2 : 10.7 called in turn, where the host's second launch counts), 1536 x 768 9.9 : 10.3,
-// 1024 x 1500 13.8 : 11.5, 2048 x 1500 15.8 : 18.9, 256 x 4999 11.7 : 10.0, 512 x 4999 15.6 : 17.7.
+// workgroup, instead of from partial rows.  Measured (us a call replayed from a graph, partial rows : beside, int8 h):
+// 256 x 768 6.4 : 3.7, 1024 x 768 6.8 : 5.9 (called in turn, where the host's second launch counts, 13.2 : 10.5),
+// 1024 x 200 7.0 : 5.8, 1024 x 1500 12.7 : 10.7, 256 x 4999 10.5 : 8.2, 100 x 15000 12.9 : 14.2; past the rule (us on
+// the GPU) 1536 x 768 9.9 : 10.3, 2048 x 1500 15.8 : 18.9, 512 x 4999 15.6 : 17.7.
 bool gain_beside(int64_t rows, int64_t n) { return rows > 0 && rows <= 1024 && !long_rows(n) && rows * n <= 3 << 19; }
 
 bool bad_size(int64_t rows, int64_t n) { return n >= (1ll << 31) - kCkptBlock || rows >= (1ll << 31); }

@@ -264,6 +264,9 @@ inline int blocks32(int n) { return (n + 31) / 32; }
 //               64 rows,  10000 x 10000: 95 % 105.9 : 91.3, 98 % 69.3 : 80.7;  2500 x 2500, 95 %: 27.1 : 23.8;
 //                         6000 x 1500: 90 % 41.4 : 38.3, 95 % 33.2 : 34.1;  3072 x 768: 90 % 19.9 : 21.8
 //              128 rows,  3072 x 768: 90 % 23.6 : 20.1, 98 % 20.4 : 19.3;  2500 x 2500: 90 % 49.4 : 35.8, 98 % 21.0 : 22.4
+// What one count of positions and one density cannot tell apart goes the slower way: dW alone at 10000 x 10000, 98 %,
+// 32 rows (22.3 : 28.0, tiles taken) and 64 (above); dX and dW at 64 rows, 768 x 3072, 90 % (25.6 : 20.2, walk taken),
+// where the transposed shape's walk is faster.
 // Operands stay below 4 GB (buffer offsets).
 constexpr int64_t kSampleBesideDx = 300000;   // positions at least, at up to 64 rows
 bool sample_layer(int64_t M, int64_t K, int64_t nnz) { return nnz > 0 && K <= kSampleMaxK && nnz >= M * K / 64; }
