@@ -282,7 +282,7 @@ snack_status pack_bf16(snack_layer* L, hipStream_t s)
         hipLaunchKernelGGL(pack_bf16_kernel, dim3(grid_for(L->nnz)), dim3(kThreads), 0, s, L->vals, L->vals16, L->nnz);
         SNACK_HIP(hipGetLastError());
     }
-    L->b16_version = L->vals_version;
+    if (!stream_capturing(s)) L->b16_version = L->vals_version;
     return SNACK_OK;
 }
 

@@ -125,6 +125,7 @@ struct snack_layer {
     // a step of vals alone was recorded into a graph: any replay may have moved
     // them past vals_t since it was last made
     bool vals_in_graph = false;
+    bool step_in_graph = false;   // a step of any kind: past the bf16 copy too
     // dW in transposed order from the last backward (bit-identical to the
     // canonical dW it was produced with); lets SGD update both value copies
     float* dwt = nullptr;

@@ -467,6 +467,7 @@ snack_status backward_sgd_impl(snack_layer* L, const float* X, const float* dY, 
 {
     SgdStep step{lr, false, false};
     ++L->vals_version;
+    if (stream_capturing(s)) L->step_in_graph = true;
     SNACK_CHECK(backward_impl(L, X, dY, dX, dW, B, s, &step, x_ready, dy_ready));
     if (!step.done) {
         // the column pass did not take the step: as snack_sgd_step would
@@ -534,7 +535,7 @@ snack_status forward_infer_one(snack_layer* L, const float* X, float* Y, int32_t
 {
     if (act != kActNone && act != kActGelu) return SNACK_ERR_INVALID_ARG;
     if (!infer_supported(L, B, b16)) return SNACK_ERR_UNSUPPORTED;
-    if (b16 && L->b16_version != L->vals_version) SNACK_CHECK(pack_bf16(L, s));
+    if (b16 && (L->b16_version != L->vals_version || L->step_in_graph)) SNACK_CHECK(pack_bf16(L, s));
     return spmm_forward_infer(L, X, Y, B, act, b16, s);
 }
 
@@ -692,7 +693,7 @@ extern "C" snack_status snack_sgd_step(snack_layer* L, const float* dW, float lr
     // next pass that reads it, never stepped with a column-order dW of its own
     L->dwt_valid = false;
     ++L->vals_version;
-    if (stream_capturing(as_stream(stream))) L->vals_in_graph = true;
+    if (stream_capturing(as_stream(stream))) L->vals_in_graph = L->step_in_graph = true;
     return sgd_update(L, dW, nullptr, lr, as_stream(stream));
 }
 

@@ -133,7 +133,9 @@ snack_status snack_forward_noalloc(snack_layer* layer, const float* X, float* Y,
  * bf16_values, a copy of them rounded to bf16, nearest even (4 bytes per
  * entry); sums are fp32.  The copy is remade by the call itself whenever the
  * values changed since it was made (training calls, drop/regrow,
- * snack_layer_values_updated).  act: 0 none, 1 the exact GELU of
+ * snack_layer_values_updated); a call captured in a HIP graph after one that made
+ * the copy reads that copy, and is captured again when the values have changed.
+ * act: 0 none, 1 the exact GELU of
  * snack_gelu_fwd, applied to each output as it is stored.  With
  * bf16_values = 0 and act = 0 the result equals snack_forward bit for bit.
  *   X device float[B, K], Y device float[B, M] (overwritten).

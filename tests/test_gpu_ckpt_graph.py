@@ -121,3 +121,40 @@ def test_captured_fused_step(M, K, nnz, B, want_dx):
     finally:
         layer.close()
         twin.close()
+
+
+def test_bf16_copy_is_made_where_it_is_read():
+    """The inference forward's 16-bit values: recording the call that makes them makes none, and a step replayed from
+    a graph moves the values past them."""
+    import numpy as np
+    import torch
+    L = lib()
+    M, K, nnz, key = 300, 260, 12000, "ckptgraph/bf16"
+    layer, twin = _layer(M, K, nnz, 2, key), _layer(M, K, nnz, 2, key)
+    try:
+        X, step = dev(normal((2, K), key + "/x")), dev(normal((nnz,), key + "/step"))
+        Y, E, T = (torch.zeros(2, M, device="cuda") for _ in range(3))
+        torch.cuda.synchronize()
+        say("bf16 capture")
+        g, gs = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            L.snack_forward_infer(layer.h, X, Y, bf16_values=True)
+        L.snack_forward_infer(layer.h, X, E, bf16_values=True)      # before the first replay
+        L.snack_forward_infer(twin.h, X, T, bf16_values=True)
+        assert torch.equal(E, T) and np.abs(host(T)).max() > 0
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, T)
+        with torch.cuda.graph(gs):
+            layer.sgd_step(step, 0.5)
+        for i in range(3):
+            say("bf16 replay", i)
+            gs.replay()
+            torch.cuda.synchronize()
+            twin.sgd_step(step, 0.5)
+            L.snack_forward_infer(layer.h, X, E, bf16_values=True)
+            L.snack_forward_infer(twin.h, X, T, bf16_values=True)
+            assert torch.equal(E, T)
+    finally:
+        layer.close()
+        twin.close()
