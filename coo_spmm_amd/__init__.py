@@ -69,6 +69,19 @@ _SIGS = {
     "snack_gelu_ckpt_fwd": ([P, i64, i64, i32, P, P, P, P, P, P], ST),
     "snack_gelu_ckpt_bwd": ([P, P, P, i64, i64, i32, P, P], ST),
     "snack_backward_ckpt": ([P, P, P, i32, P, P, P, i32, P], ST),
+    "snack_rope_table": ([i32, i32, f64, f64, f64, f64, f64, f64, P, P], ST),
+    "snack_qk_rope_fwd": ([P, i64, i64, i32, P, i64, i64, i32, i32, i64, i32, P, P, P, P, f32, P, P, i32, P], ST),
+    "snack_qk_rope_bwd_work": ([i64, i32, i32, i32, ctypes.POINTER(i64)], ST),
+    "snack_qk_rope_bwd": ([P, i64, i64, i32, P, i64, i64, i32, i32, i64, i32, P, P, P, P, f32, P, i64, i64, P, i64, i64,
+                           i32, P, P, P, P, P, i64, P], ST),
+    "snack_cache_bytes": ([P, ctypes.POINTER(i64)], ST),
+    "snack_cache_slots": ([P, P, i32, P, P, i32, i64, P, P, P], ST),
+    "snack_cache_write": ([P, P, i64, i64, P, i64, i64, i32, i64, P, P], ST),
+    "snack_cache_write_rope": ([P, P, i64, i64, i32, P, i64, i64, P, i64, i64, i32, i64, P, P, P, P, P, f32, P, i32, P],
+                               ST),
+    "snack_cache_read": ([P, P, i64, P, P, i32, P], ST),
+    "snack_cache_attend_work": ([P, i32, i64, i32, ctypes.POINTER(i64)], ST),
+    "snack_cache_attend": ([P, P, i64, i64, i32, i32, i64, P, i32, P, P, i32, f32, i32, P, P, i64, P], ST),
     "snack_profile_enable": ([ctypes.c_int], ST),
     "snack_profile_reset": ([], ST),
     "snack_profile_name": ([ctypes.c_int], ctypes.c_char_p),
@@ -110,6 +123,17 @@ def _ptr(t):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("tensors passed to the library must be contiguous device tensors")
     return t.data_ptr()
+
+
+def _spread(t):
+    """Address, elements from token to token and from head to head of [tokens, heads, features]."""
+    if t is None:
+        return None, 0, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch tensor")
+    if not t.is_cuda or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError("heads must be [tokens, heads, features] on the GPU, their features contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1)
 
 
 def _stream(stream=None):
@@ -343,6 +367,93 @@ def snack_backward_ckpt(h, Q, S, fmt, dY, dX=None, dW=None, stream=None):
     B = dY.shape[0]
     _check(_lib.snack_backward_ckpt(h, _ptr(Q), _ptr(S), fmt, _ptr(dY), _ptr(dX), _ptr(dW), B, _stream(stream)),
            "snack_backward_ckpt")
+
+
+E2M1 = 4                      # 4-bit numbers, of a cache only
+ROPE_HALF, ROPE_PAIRS = 0, 1
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", P), ("positions", i32), ("rot", i32), ("layout", i32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("data", P), ("pages", i64), ("page_tokens", i32), ("heads", i32), ("head_dim", i32), ("fmt", i32)]
+
+
+def snack_rope_table(positions, rot, base, factor, trained, low, high, amplitude, table, stream=None):
+    """table: float32 [positions, rot], written."""
+    _need(table, torch.float32, (positions, rot), "table")
+    _check(_lib.snack_rope_table(positions, rot, base, factor, trained, low, high, amplitude, _ptr(table),
+                                 _stream(stream)), "snack_rope_table")
+
+
+def snack_qk_rope_fwd(q, k, x_fmt, pos, rope, q_gain, k_gain, eps, Yq, Yk, y_fmt, stream=None):
+    """q, k: [tokens, heads, features] device tensors, each row of features contiguous (k may be None); rope: the
+    address of a snack_rope, or None."""
+    t, hq, d = q.shape
+    _check(_lib.snack_qk_rope_fwd(*_spread(q), hq, *_spread(k), 0 if k is None else k.shape[1], x_fmt, t, d, _ptr(pos),
+                                  rope, _ptr(q_gain), _ptr(k_gain), eps, _ptr(Yq), _ptr(Yk), y_fmt, _stream(stream)),
+           "snack_qk_rope_fwd")
+
+
+@functools.lru_cache(maxsize=256)   # a function of the shape alone
+def snack_qk_rope_bwd_work(tokens, q_heads, k_heads, head_dim):
+    b = i64()
+    _check(_lib.snack_qk_rope_bwd_work(tokens, q_heads, k_heads, head_dim, ctypes.byref(b)), "snack_qk_rope_bwd_work")
+    return b.value
+
+
+def snack_qk_rope_bwd(q, k, x_fmt, pos, rope, q_gain, k_gain, eps, dYq, dYk, y_fmt, dXq, dXk, dq_gain, dk_gain, work,
+                      stream=None):
+    """work: a device tensor of at least snack_qk_rope_bwd_work bytes, or None."""
+    t, hq, d = dYq.shape
+    nbytes = 0 if work is None else work.numel() * work.element_size()
+    _check(_lib.snack_qk_rope_bwd(*_spread(q), hq, *_spread(k), 0 if dYk is None else dYk.shape[1], x_fmt, t, d,
+                                  _ptr(pos), rope, _ptr(q_gain), _ptr(k_gain), eps, *_spread(dYq), *_spread(dYk), y_fmt,
+                                  _ptr(dXq), _ptr(dXk), _ptr(dq_gain), _ptr(dk_gain), _ptr(work), nbytes,
+                                  _stream(stream)), "snack_qk_rope_bwd")
+
+
+def snack_cache_bytes(cache):
+    """cache: the address of a snack_cache (here and below)."""
+    b = i64()
+    _check(_lib.snack_cache_bytes(cache, ctypes.byref(b)), "snack_cache_bytes")
+    return b.value
+
+
+def snack_cache_slots(cache, table, lens, starts, pos, slot, stream=None):
+    _check(_lib.snack_cache_slots(cache, _ptr(table), table.shape[1], _ptr(lens), _ptr(starts), table.shape[0],
+                                  pos.numel(), _ptr(pos), _ptr(slot), _stream(stream)), "snack_cache_slots")
+
+
+def snack_cache_write(cache, k, v, x_fmt, slot, stream=None):
+    _check(_lib.snack_cache_write(cache, *_spread(k), *_spread(v), x_fmt, slot.numel(), _ptr(slot), _stream(stream)),
+           "snack_cache_write")
+
+
+def snack_cache_write_rope(cache, q, k, v, x_fmt, pos, slot, rope, q_gain, k_gain, eps, Yq, y_fmt, stream=None):
+    _check(_lib.snack_cache_write_rope(cache, *_spread(q), q.shape[1], *_spread(k), *_spread(v), x_fmt, slot.numel(),
+                                       _ptr(pos), _ptr(slot), rope, _ptr(q_gain), _ptr(k_gain), eps, _ptr(Yq), y_fmt,
+                                       _stream(stream)), "snack_cache_write_rope")
+
+
+def snack_cache_read(cache, slot, K, V, y_fmt, stream=None):
+    _check(_lib.snack_cache_read(cache, _ptr(slot), slot.numel(), _ptr(K), _ptr(V), y_fmt, _stream(stream)),
+           "snack_cache_read")
+
+
+def snack_cache_attend_work(cache, q_heads, tokens, sequences):
+    b = i64()
+    _check(_lib.snack_cache_attend_work(cache, q_heads, tokens, sequences, ctypes.byref(b)), "snack_cache_attend_work")
+    return b.value
+
+
+def snack_cache_attend(cache, q, q_fmt, table, lens, starts, scale, causal, out, work, stream=None):
+    _check(_lib.snack_cache_attend(cache, *_spread(q), q.shape[1], q_fmt, q.shape[0], _ptr(table), table.shape[1],
+                                   _ptr(lens), _ptr(starts), table.shape[0], scale, 1 if causal else 0, _ptr(out),
+                                   _ptr(work), work.numel() * work.element_size(), _stream(stream)),
+           "snack_cache_attend")
 
 
 def snack_profile_enable(on=True):
@@ -622,6 +733,322 @@ def gelu_ckpt_bwd(ck, dY, stream=None):
     _check(_lib.snack_gelu_ckpt_bwd(q, s, pd, ck.rows, ck.n, ck.fmt, dX.data_ptr(), _raw_stream(dev)),
            "snack_gelu_ckpt_bwd")
     return dX
+
+
+# ---------------------------------------------------------------------------
+# The attention half of a block: norms and rotation of queries and keys, the cache, the attention over it
+# ---------------------------------------------------------------------------
+
+def _heads(t, name, dev=None, dtype=None, shape=None):
+    """Address, token stride and head stride of t, [tokens, heads, features] on the current GPU (or on GPU `dev`), each
+    row of features contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype not in _HIDDEN or (dtype is not None and t.dtype is not dtype):
+        raise TypeError(f"{name} must be {dtype if dtype is not None else 'float32 or bfloat16'}, got {t.dtype}")
+    if shape is None:
+        if t.dim() != 3 or not 1 <= t.shape[2] <= 256 or t.shape[1] < 1:
+            raise ValueError(f"{name} must be [tokens, heads, features] of at most 256 features, got {tuple(t.shape)}")
+    elif t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    on = t.get_device()
+    if dev is None:
+        if on < 0 or on != torch._C._cuda_getDevice():
+            raise ValueError(f"{name} must be on the current GPU")
+    elif on != dev:
+        raise ValueError(f"{name} must be on the same GPU as the other tensors")
+    row, head, one = t.stride()
+    if one != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name} must have contiguous features")
+    return t.data_ptr(), row, head
+
+
+class RopeTable:
+    """The table of rotary positions: float32 [positions, rot], for every position the cosines of rot / 2 angles, then
+    their sines; the first rot features of a head are rotated.  layout: ROPE_HALF (feature i turns with i + rot / 2) or
+    ROPE_PAIRS (feature 2 i with 2 i + 1)."""
+
+    __slots__ = ("table", "layout", "_c", "_ref")
+
+    def __init__(self, table, layout=ROPE_HALF):
+        positions, rot, p, _ = _rows(table, "table")
+        if rot % 2 or rot > 256:
+            raise ValueError("an even number of features, at most 256, is rotated")
+        if positions < 1 or layout not in (ROPE_HALF, ROPE_PAIRS):
+            raise ValueError("a table has a position at least, and the layout ROPE_HALF or ROPE_PAIRS")
+        self.table, self.layout = table, layout
+        self._c = _Rope(p, positions, rot, layout)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def make(cls, positions, rot, base=10000.0, layout=ROPE_HALF, factor=1.0, trained=0.0, low=1.0, high=32.0,
+             amplitude=1.0, stream=None):
+        """cos and sin of p f_i, f_i = base^(-2 i / rot), times amplitude, on the current GPU.  For contexts `factor`
+        times as long as the trained one: every f_i / factor, or with `trained` (its tokens) only those of pairs that
+        make at most `low` turns in it; of at least `high` turns f_i stays, in between it is interpolated."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return cls.make(positions, rot, base, layout, factor, trained, low, high, amplitude)
+        if positions < 1 or rot < 2:
+            raise ValueError("a table has a position and a pair at least")
+        table = torch.empty((positions, rot), dtype=_FLOAT, device=torch.cuda.current_device())
+        rope = cls(table, layout)
+        _check(_lib.snack_rope_table(positions, rot, base, factor, trained, low, high, amplitude, table.data_ptr(),
+                                     _raw_stream(table.get_device())), "snack_rope_table")
+        return rope
+
+    @property
+    def positions(self):
+        return self._c.positions
+
+    @property
+    def rot(self):
+        return self._c.rot
+
+    def _on(self, dev):
+        if self.table.get_device() != dev:
+            raise ValueError("the rotation's table must be on the same GPU as the other tensors")
+        return self._ref
+
+
+def _qk_args(pos, rope, q_gain, k_gain, tokens, d, dev):
+    """Addresses of what norm and rotation take beside the heads."""
+    if rope is None and q_gain is None and k_gain is None:
+        raise ValueError("neither a rotation nor a gain is given")
+    pp = pr = None
+    if rope is not None:
+        if rope.rot > d:
+            raise ValueError(f"the rotation is of {rope.rot} features, a head has {d}")
+        pr = rope._on(dev)
+        pp = _arg(pos, (tokens,), "pos", dev, torch.int32)
+    gq = None if q_gain is None else _arg(q_gain, (d,), "q_gain", dev)
+    gk = None if k_gain is None else _arg(k_gain, (d,), "k_gain", dev)
+    return pp, pr, gq, gk
+
+
+def qk_rope_fwd(q, k, pos=None, rope=None, q_gain=None, k_gain=None, eps=1e-6, dtype=None, stream=None):
+    """Norms of queries and keys for each head, y = x / sqrt(mean(x^2) + eps) * gain, then the rotation of y by the
+    tokens' positions pos (int32 [tokens]).
+
+    q, k: float32 or bfloat16 [tokens, heads, features], as they lie in the projections' output (each head's features
+    contiguous); k may be None.  rope: a RopeTable, None for none; q_gain, k_gain: float32 [features], None: those heads
+    are not normed.  Returns (q', k') in dtype (None: q's)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_rope_fwd(q, k, pos, rope, q_gain, k_gain, eps, dtype)
+    aq = _heads(q, "q")
+    t, hq, d = q.shape
+    dev = q.get_device()
+    y_fmt = _HIDDEN.get(q.dtype if dtype is None else dtype)
+    if y_fmt is None:
+        raise TypeError("queries and keys are written as float32 or bfloat16")
+    pp, pr, gq, gk = _qk_args(pos, rope, q_gain, k_gain, t, d, dev)
+    yq = torch.empty((t, hq, d), dtype=q.dtype if dtype is None else dtype, device=q.device)
+    ak, hk, yk, pk = (None, 0, 0), 0, None, None
+    if k is not None:
+        hk = k.shape[1] if k.dim() == 3 else 1
+        ak = _heads(k, "k", dev, q.dtype, (t, hk, d))
+        if hk < 1:
+            raise ValueError("k must have a head at least")
+        yk = torch.empty((t, hk, d), dtype=yq.dtype, device=q.device)
+        pk = yk.data_ptr()
+    _check(_lib.snack_qk_rope_fwd(*aq, hq, *ak, hk, _HIDDEN[q.dtype], t, d, pp, pr, gq, gk, eps, yq.data_ptr(), pk,
+                                  y_fmt, _raw_stream(dev)), "snack_qk_rope_fwd")
+    return yq, yk
+
+
+def qk_rope_bwd(q, k, pos, dq, dk, rope=None, q_gain=None, k_gain=None, eps=1e-6, stream=None):
+    """The gradient of qk_rope_fwd from those of its outputs, dq and dk (float32 or bfloat16, each head's features
+    contiguous; k and dk None for none).  Returns (gradient of q, of k, of q_gain, of k_gain), None where there is no
+    such input."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qk_rope_bwd(q, k, pos, dq, dk, rope, q_gain, k_gain, eps)
+    aq = _heads(q, "q")
+    t, hq, d = q.shape
+    dev = q.get_device()
+    adq = _heads(dq, "dq", dev, None, (t, hq, d))
+    pp, pr, gq, gk = _qk_args(pos, rope, q_gain, k_gain, t, d, dev)
+    dxq = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+    ak = adk = (None, 0, 0)
+    hk, dxk, pk = 0, None, None
+    if (k is None) != (dk is None):
+        raise ValueError("k and dk must both be given, or neither")
+    if k is not None:
+        hk = k.shape[1] if k.dim() == 3 else 1
+        ak = _heads(k, "k", dev, q.dtype, (t, hk, d))
+        adk = _heads(dk, "dk", dev, dq.dtype, (t, hk, d))
+        if hk < 1:
+            raise ValueError("k must have a head at least")
+        dxk = torch.empty((t, hk, d), dtype=q.dtype, device=q.device)
+        pk = dxk.data_ptr()
+    elif k_gain is not None:
+        raise ValueError("k_gain is given without k")
+    dgq = None if q_gain is None else torch.empty_like(q_gain)
+    dgk = None if k_gain is None else torch.empty_like(k_gain)
+    work, nbytes, pw = None, 0, None
+    if dgq is not None or dgk is not None:
+        nbytes = snack_qk_rope_bwd_work(t, hq, hk, d)
+        work = q.new_empty(nbytes, dtype=_BYTE)
+        pw = work.data_ptr()
+    _check(_lib.snack_qk_rope_bwd(*aq, hq, *ak, hk, _HIDDEN[q.dtype], t, d, pp, pr, gq, gk, eps, *adq, *adk,
+                                  _HIDDEN[dq.dtype], dxq.data_ptr(), pk, None if dgq is None else dgq.data_ptr(),
+                                  None if dgk is None else dgk.data_ptr(), pw, nbytes, _raw_stream(dev)),
+           "snack_qk_rope_bwd")
+    return dxq, dxk, dgq, dgk
+
+
+class KVCache:
+    """Keys and values of attention heads kept in 8 bits (INT8, E4M3) or 4 (E2M1), with an exponent byte for every 32
+    features of a token's head, in pages of `page` tokens (a multiple of 32).
+
+    A token's place is its slot, page * tokens of a page + offset; which pages are a sequence's says a page table, int32
+    [sequences, width]; lens, int32 [sequences], are the sequences' tokens in the cache with those of the call.  A call's
+    tokens are the newest of every sequence, one sequence after the other: starts, int32 [sequences + 1], says where each
+    begins (None: equally many of every sequence).  data: uint8 of KVCache.nbytes_of(...) bytes, or None (allocated; not
+    cleared: what no token was written to may hold anything)."""
+
+    __slots__ = ("data", "_c", "_ref", "_dev", "_work")
+
+    def __init__(self, pages, heads, head_dim, fmt, page=64, data=None):
+        self._c = _Cache(None, pages, page, heads, head_dim, fmt)
+        self._ref = ctypes.addressof(self._c)
+        nbytes = snack_cache_bytes(self._ref)
+        if data is None:
+            data = torch.empty(nbytes, dtype=_BYTE, device=torch.cuda.current_device())
+        elif not isinstance(data, torch.Tensor) or data.get_device() < 0:
+            raise TypeError("data must be a tensor on the GPU")
+        self._dev = data.get_device()
+        self._c.data = _arg(data, (nbytes,), "data", self._dev, _BYTE)
+        self.data, self._work = data, {}
+        self._on()
+
+    @staticmethod
+    def nbytes_of(pages, heads, head_dim, fmt, page=64):
+        c = _Cache(None, pages, page, heads, head_dim, fmt)
+        return snack_cache_bytes(ctypes.addressof(c))
+
+    pages = property(lambda self: self._c.pages)
+    page = property(lambda self: self._c.page_tokens)
+    heads = property(lambda self: self._c.heads)
+    head_dim = property(lambda self: self._c.head_dim)
+    fmt = property(lambda self: self._c.fmt)
+    nbytes = property(lambda self: self.data.numel())
+
+    def _on(self):
+        if self._dev != torch._C._cuda_getDevice():
+            raise ValueError("the cache must be on the current GPU")
+        return self._dev
+
+    def _sequences(self, table, lens, starts, dev):
+        if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.shape[1] < 1:
+            raise ValueError("table must be [sequences, pages]")
+        n, width = table.shape
+        return (_arg(table, table.shape, "table", dev, torch.int32), width, _arg(lens, (n,), "lens", dev, torch.int32),
+                None if starts is None else _arg(starts, (n + 1,), "starts", dev, torch.int32), n)
+
+    def slots(self, table, lens, tokens, starts=None, stream=None):
+        """(pos, slot): position (int32) and place in the cache (int64) of a call's tokens; slot -1 where there is none.
+        The same for every block of a model."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.slots(table, lens, tokens, starts)
+        dev = self._on()
+        pt, width, pl, ps, n = self._sequences(table, lens, starts, dev)
+        if starts is None and (n == 0 or tokens % n):
+            raise ValueError("without starts the tokens must divide among the sequences")
+        pos = torch.empty(tokens, dtype=torch.int32, device=table.device)
+        slot = torch.empty(tokens, dtype=torch.int64, device=table.device)
+        _check(_lib.snack_cache_slots(self._ref, pt, width, pl, ps, n, tokens, pos.data_ptr(), slot.data_ptr(),
+                                      _raw_stream(dev)), "snack_cache_slots")
+        return pos, slot
+
+    def write(self, k, v, slot, stream=None):
+        """Keep keys and values, float32 or bfloat16 [tokens, heads, features], at distinct slots (int64 [tokens]; those
+        outside the cache are not written)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.write(k, v, slot)
+        dev = self._on()
+        t = slot.shape[0] if isinstance(slot, torch.Tensor) and slot.dim() else 0
+        ps = _arg(slot, (t,), "slot", dev, torch.int64)
+        shape = (t, self._c.heads, self._c.head_dim)
+        ak = _heads(k, "k", dev, None, shape)
+        av = _heads(v, "v", dev, k.dtype, shape)
+        _check(_lib.snack_cache_write(self._ref, *ak, *av, _HIDDEN[k.dtype], t, ps, _raw_stream(dev)),
+               "snack_cache_write")
+
+    def write_rope(self, q, k, v, pos, slot, rope=None, q_gain=None, k_gain=None, eps=1e-6, dtype=None, stream=None):
+        """qk_rope_fwd whose keys go into the cache, the values with them, in one launch.  Returns q'."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.write_rope(q, k, v, pos, slot, rope, q_gain, k_gain, eps, dtype)
+        dev = self._on()
+        aq = _heads(q, "q", dev)
+        t, hq, d = q.shape
+        if d != self._c.head_dim:
+            raise ValueError(f"a head of the cache has {self._c.head_dim} features, got {d}")
+        shape = (t, self._c.heads, d)
+        ak, av = _heads(k, "k", dev, q.dtype, shape), _heads(v, "v", dev, q.dtype, shape)
+        y_fmt = _HIDDEN.get(q.dtype if dtype is None else dtype)
+        if y_fmt is None:
+            raise TypeError("queries are written as float32 or bfloat16")
+        pp, pr, gq, gk = _qk_args(pos, rope, q_gain, k_gain, t, d, dev)
+        ps = _arg(slot, (t,), "slot", dev, torch.int64)
+        yq = torch.empty((t, hq, d), dtype=q.dtype if dtype is None else dtype, device=q.device)
+        _check(_lib.snack_cache_write_rope(self._ref, *aq, hq, *ak, *av, _HIDDEN[q.dtype], t, pp, ps, pr, gq, gk, eps,
+                                           yq.data_ptr(), y_fmt, _raw_stream(dev)), "snack_cache_write_rope")
+        return yq
+
+    def read(self, slot, dtype=torch.float32, stream=None):
+        """(keys, values) that the cache stands for at slots (int64 [tokens]), [tokens, heads, features] in float32 or
+        bfloat16; zeros at a negative slot, NaN past the cache."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.read(slot, dtype)
+        dev = self._on()
+        y_fmt = _HIDDEN.get(dtype)
+        if y_fmt is None:
+            raise TypeError("a cache is read as float32 or bfloat16")
+        t = slot.shape[0] if isinstance(slot, torch.Tensor) and slot.dim() else 0
+        ps = _arg(slot, (t,), "slot", dev, torch.int64)
+        shape = (t, self._c.heads, self._c.head_dim)
+        k = torch.empty(shape, dtype=dtype, device=slot.device)
+        v = torch.empty(shape, dtype=dtype, device=slot.device)
+        _check(_lib.snack_cache_read(self._ref, ps, t, k.data_ptr(), v.data_ptr(), y_fmt, _raw_stream(dev)),
+               "snack_cache_read")
+        return k, v
+
+    def attend(self, q, table, lens, starts=None, scale=None, causal=True, out=None, stream=None):
+        """softmax(scale q . k) v over the tokens of each query's sequence, those up to its own with `causal` (else all:
+        an encoder's states).  q: float32 or bfloat16 [tokens, query heads, features], each head's features contiguous,
+        query heads a multiple of the cache's; scale: 1 / sqrt(features) if None.  Returns out (contiguous, of q's type
+        and shape); a query that sees no token gets 0, rows of no sequence are not written."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.attend(q, table, lens, starts, scale, causal, out)
+        dev = self._on()
+        aq = _heads(q, "q", dev)
+        t, hq, d = q.shape
+        if d != self._c.head_dim or hq % self._c.heads:
+            raise ValueError(f"q must have heads of {self._c.head_dim} features, a multiple of {self._c.heads} of them")
+        pt, width, pl, ps, n = self._sequences(table, lens, starts, dev)
+        if starts is None and (n == 0 or t % n):
+            raise ValueError("without starts the tokens must divide among the sequences")
+        if out is None:
+            out = torch.empty((t, hq, d), dtype=q.dtype, device=q.device)
+        po = _arg(out, (t, hq, d), "out", dev, q.dtype)
+        key = (hq, t, n)
+        nbytes = self._work.get(key)
+        if nbytes is None:
+            if len(self._work) >= 256:
+                self._work.clear()
+            nbytes = self._work[key] = snack_cache_attend_work(self._ref, hq, t, n)
+        work = q.new_empty(nbytes, dtype=_BYTE)
+        _check(_lib.snack_cache_attend(self._ref, *aq, hq, _HIDDEN[q.dtype], t, pt, width, pl, ps, n,
+                                       d ** -0.5 if scale is None else scale, 1 if causal else 0, po, work.data_ptr(),
+                                       nbytes, _raw_stream(dev)), "snack_cache_attend")
+        return out
 
 
 # ---------------------------------------------------------------------------

@@ -35,6 +35,9 @@ enum KernelClass : int {
     KC_PRUNE,
     KC_CKPT,
     KC_NORM,
+    KC_ROPE,
+    KC_CACHE,
+    KC_ATTEND,
     KC_COUNT
 };
 

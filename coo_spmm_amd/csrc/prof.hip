@@ -27,7 +27,8 @@ std::map<std::pair<int, int64_t>, std::pair<int64_t, double>> g_tagged;
 
 const char* const g_names[KC_COUNT] = {"spmm_forward", "spmm_dx", "sddmm_dw", "transpose", "vals_t_refresh",
                                        "sgd", "elementwise", "radix_sort", "canonicalise", "prune_regrow",
-                                       "checkpoint", "rmsnorm"};
+                                       "checkpoint", "rmsnorm", "qk_rope", "kv_cache",
+                                       "attend"};
 
 hipEvent_t get_event()
 {

@@ -1,0 +1,316 @@
+// rope.hip -- the table of the rotary positions, and the gradient of the norms and
+// the rotation of queries and keys (the forward pass is cache.hip's: the same
+// kernel also writes the cache).
+//
+//   y = x rstd gain for each head, rstd = 1 / sqrt(mean(x^2) + eps), then turned
+//   dy = the gradient turned back, xh = x rstd, w = dy gain
+//   dx = rstd (w - xh mean(w xh)),   dgain = sum over tokens and heads of dy xh
+//
+// One pass over x, the gradient and dx, which bounds it.  A head lies on a group of
+// lanes, eight features each, so its two sums are a few DPP steps.  A workgroup
+// takes a run of heads and adds up their terms of dgain in registers, in order; the
+// partial rows of the workgroups are added up by a second launch in a fixed tree.
+#include "rope.h"
+
+#include <math.h>
+
+namespace snack {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxGroups = 2048;    // workgroups (and partial rows) of a gradient at most
+constexpr int kSumThreads = 1024;
+
+__global__ void __launch_bounds__(kThreads) table_kernel(float* __restrict__ T, uint32_t total, FastDiv by_r,
+                                                         double log2_base, double factor, double trained, double low,
+                                                         double high, double amplitude)
+{
+    const uint32_t id = blockIdx.x * kThreads + threadIdx.x;
+    if (id >= total) return;
+    const int r = (int)by_r.d;
+    const uint32_t p = fast_quot(by_r, id), i = id - p * by_r.d;
+    double f = exp2(-log2_base * (double)i / (double)r);
+    double w = 0.0;
+    if (trained > 0.0) w = fmin(fmax((trained * f * 0.15915494309189535 - low) / (high - low), 0.0), 1.0);
+    f *= w + (1.0 - w) / factor;
+    double s, c;
+    sincos((double)p * f, &s, &c);
+    float* row = T + (int64_t)p * (2 * r);
+    row[i] = (float)(c * amplitude);
+    row[r + i] = (float)(s * amplitude);
+}
+
+struct BwdPart {
+    Heads x, g;          // x (p null: not read) and the gradient of y
+    const float* gain;   // null: not normed
+    void* dx;
+    float* part;         // partial rows of dgain [groups][d], or null
+    uint32_t groups;     // workgroups
+    uint32_t run;        // heads (rows) of a workgroup
+};
+
+template <int LPR, typename X, typename Y>
+__global__ void __launch_bounds__(kThreads)
+qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rotation ro, double eps, double inv_d)
+{
+    __shared__ float sums[kThreads * 8];
+    const bool second = blockIdx.x >= q.groups;
+    const BwdPart& a = second ? k : q;
+    const uint32_t group = second ? blockIdx.x - q.groups : blockIdx.x;
+    constexpr int kRows = kThreads / LPR;
+    const int lane = (int)threadIdx.x % LPR, f0 = 8 * lane;
+    const uint32_t first = group * a.run, last = min(a.x.rows, first + a.run);
+    f32x8 dg = {0, 0, 0, 0, 0, 0, 0, 0};
+    // whole wavefronts stay in the loop: the sums over lanes take every lane
+    for (uint32_t at = first; at < last; at += kRows) {
+        const uint32_t row = at + threadIdx.x / LPR;
+        const bool live = row < last;
+        const uint32_t rr = live ? row : last - 1;
+        const uint32_t token = fast_quot(a.x.heads, rr), h = rr - token * a.x.heads.d;
+        const Y* gp = (const Y*)a.g.p + (int64_t)token * a.g.row + (int64_t)h * a.g.head;
+        f32x8 dy = load8(gp + f0, d - f0);
+        f32x8 x = {0, 0, 0, 0, 0, 0, 0, 0}, gain = x;
+        if (a.gain) {
+            x = load8((const X*)a.x.p + (int64_t)token * a.x.row + (int64_t)h * a.x.head + f0, d - f0);
+            gain = load8(a.gain + f0, d - f0);
+        }
+        if (ro.table) {
+            const int p = pos[token];
+            if (f0 < 2 * ro.r) {
+                const Turn t = load_turn(ro, p, f0, true);
+                const f32x8 o = ro.layout == SNACK_ROPE_PAIRS ? swap_pairs(dy) : load_partners(ro, gp, f0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dy[i] = f0 + i < 2 * ro.r ? fmaf(o[i], t.s[i], dy[i] * t.c[i]) : dy[i] * t.c[i];
+            } else if ((uint32_t)p >= ro.positions) {
+                dy *= __builtin_nanf("");
+            }
+        }
+        f32x8 dx = dy;
+        if (a.gain) {
+            const f32x8 w = dy * gain;
+            // 64 bits: squares of any fp32 value
+            double ss = 0.0, ws = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                ss = fma((double)x[i], (double)x[i], ss);
+                ws = fma((double)w[i], (double)x[i], ws);
+            }
+            const double r = rsqrt64(fma(lanes_sum<LPR>(ss), inv_d, eps));
+            const float rstd = (float)r;
+            const float m = (float)(lanes_sum<LPR>(ws) * inv_d * r * r);
+            const f32x8 xh = x * rstd;
+            if (live) dg += dy * xh;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dx[i] = rstd * fmaf(-x[i], m, w[i]);
+        }
+        if (live) store8((X*)a.dx + (int64_t)row * d + f0, dx, d - f0);
+    }
+    if (!a.part) return;
+    // the lanes of a feature: kRows of them, in order
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[i * kThreads + (int)threadIdx.x] = dg[i];
+    __syncthreads();
+    for (int f = (int)threadIdx.x; f < d; f += kThreads) {
+        float s = 0.0f;
+        for (int j = 0; j < kRows; ++j) s += sums[(f & 7) * kThreads + j * LPR + (f >> 3)];
+        a.part[(int64_t)group * d + f] = s;
+    }
+}
+
+// dgain[f] = sum over the partial rows, in 64 bits; a workgroup 32 features, its threads 32 runs of rows each
+__global__ void __launch_bounds__(kSumThreads)
+gain_sum_kernel(const float* __restrict__ pq, uint32_t nq, float* __restrict__ gq, const float* __restrict__ pk,
+                uint32_t nk, float* __restrict__ gk, int d)
+{
+    __shared__ double sums[32][33];
+    const bool second = blockIdx.y != 0;
+    const float* p = second ? pk : pq;
+    const uint32_t n = second ? nk : nq;
+    float* out = second ? gk : gq;
+    if (!out) return;
+    const int c = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5, f = (int)blockIdx.x * 32 + c;
+    double s = 0.0;
+    if (f < d)
+        for (uint32_t i = r; i < n; i += 32) s += p[(int64_t)i * d + f];
+    sums[r][c] = s;
+    __syncthreads();
+    if (r == 0 && f < d) {
+        double t = 0.0;
+        for (int i = 0; i < 32; ++i) t += sums[i][c];
+        out[f] = (float)t;
+    }
+}
+
+// workgroups of `rows` heads and the heads of each
+void bwd_split(uint32_t rows, int d, uint32_t most, uint32_t* groups, uint32_t* run)
+{
+    const uint32_t per = kThreads / head_lanes(d);
+    const uint32_t units = (rows + per - 1) / per;     // rows a workgroup takes at once
+    const uint32_t turns = units ? (units + most - 1) / most : 0;
+    *run = turns * per;
+    *groups = turns ? (units + turns - 1) / turns : 0;
+}
+// of queries and keys: the workgroups shared out by their heads
+void bwd_splits(uint32_t rq, uint32_t rk, int d, uint32_t* gq, uint32_t* runq, uint32_t* gk, uint32_t* runk)
+{
+    const uint64_t all = (uint64_t)rq + rk;
+    const uint32_t mq = all ? (uint32_t)((uint64_t)kMaxGroups * rq / all) : 0;
+    bwd_split(rq, d, mq < 1 ? 1 : mq, gq, runq);
+    bwd_split(rk, d, kMaxGroups - mq < 1 ? 1 : kMaxGroups - mq, gk, runk);
+}
+
+}  // namespace
+
+snack_status make_heads(const void* p, int64_t row, int64_t head, int32_t heads, int64_t tokens, int32_t d, int32_t fmt,
+                        Heads* out)
+{
+    if (heads < 0 || tokens < 0 || d < 1 || d > 256 || !float_format(fmt)) return SNACK_ERR_INVALID_ARG;
+    if (tokens >= (1ll << 31) || tokens * heads >= (1ll << 31)) return SNACK_ERR_UNSUPPORTED;
+    out->p = p;
+    out->row = row;
+    out->head = head;
+    out->heads = fast_div((uint32_t)(heads < 1 ? 1 : heads));
+    out->rows = (uint32_t)(tokens * heads);
+    if (out->rows && misaligned(p, fmt == SNACK_F32 ? 4 : 2)) return SNACK_ERR_INVALID_ARG;
+    return SNACK_OK;
+}
+
+snack_status make_rotation(const snack_rope* rope, int32_t d, const int32_t* pos, int64_t tokens, Rotation* out)
+{
+    *out = Rotation{nullptr, 0, 0, 0};
+    if (!rope) return SNACK_OK;
+    if (!rope->table || rope->positions < 1 || rope->rot < 2 || rope->rot % 2 || rope->rot > d || (tokens && !pos))
+        return SNACK_ERR_INVALID_ARG;
+    if (rope->layout != SNACK_ROPE_HALF && rope->layout != SNACK_ROPE_PAIRS) return SNACK_ERR_INVALID_ARG;
+    if (misaligned(rope->table, 4) || misaligned(pos, 4)) return SNACK_ERR_INVALID_ARG;
+    *out = Rotation{rope->table, (uint32_t)rope->positions, rope->rot / 2, rope->layout};
+    return SNACK_OK;
+}
+
+}  // namespace snack
+
+using namespace snack;
+
+extern "C" snack_status snack_rope_table(int32_t positions, int32_t rot, double base, double factor, double trained,
+                                         double low, double high, double amplitude, float* table, snack_stream stream)
+{
+    if (positions < 1 || rot < 2 || rot % 2 || rot > 256 || !table || misaligned(table, 4)) return SNACK_ERR_INVALID_ARG;
+    if (!(base > 0) || !(factor > 0) || !(trained >= 0) || !(low < high) || !isfinite(base) || !isfinite(factor) ||
+        !isfinite(trained) || !isfinite(low) || !isfinite(high) || !isfinite(amplitude))
+        return SNACK_ERR_INVALID_ARG;
+    const int64_t total = (int64_t)positions * (rot / 2);
+    if (total >= (1ll << 31)) return SNACK_ERR_UNSUPPORTED;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    ProfScope prof(KC_ROPE, s);
+    hipLaunchKernelGGL(table_kernel, dim3((unsigned)((total + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, table,
+                       (uint32_t)total, fast_div((uint32_t)(rot / 2)), log2(base), factor, trained, low, high,
+                       amplitude);
+    SNACK_HIP(hipGetLastError());
+    return SNACK_OK;
+}
+
+extern "C" snack_status snack_qk_rope_fwd(const void* Q, int64_t q_row, int64_t q_head, int32_t q_heads, const void* K,
+                                          int64_t k_row, int64_t k_head, int32_t k_heads, int32_t x_fmt,
+                                          int64_t tokens, int32_t head_dim, const int32_t* pos, const snack_rope* rope,
+                                          const float* q_gain, const float* k_gain, float eps, void* Yq, void* Yk,
+                                          int32_t y_fmt, snack_stream stream)
+{
+    QkPass a{};
+    SNACK_CHECK(make_heads(Q, q_row, q_head, q_heads, tokens, head_dim, x_fmt, &a.q));
+    SNACK_CHECK(make_heads(K, k_row, k_head, k_heads, tokens, head_dim, x_fmt, &a.k));
+    SNACK_CHECK(make_rotation(rope, head_dim, pos, tokens, &a.ro));
+    if (!float_format(y_fmt) || !(eps >= 0) || !isfinite(eps)) return SNACK_ERR_INVALID_ARG;
+    if (tokens == 0) return SNACK_OK;
+    const uintptr_t ya = y_fmt == SNACK_F32 ? 4 : 2;
+    if ((a.q.rows && (!Q || !Yq || misaligned(Yq, ya))) || (a.k.rows && (!K || !Yk || misaligned(Yk, ya))) ||
+        misaligned(q_gain, 4) || misaligned(k_gain, 4) || a.q.rows + (uint64_t)a.k.rows == 0)
+        return SNACK_ERR_INVALID_ARG;
+    a.d = head_dim;
+    a.pos = pos;
+    a.q_gain = q_gain;
+    a.k_gain = k_gain;
+    a.eps = (double)eps;
+    a.yq = Yq;
+    a.yk = Yk;
+    return qk_pass(a, nullptr, 0, x_fmt, y_fmt, KC_ROPE, reinterpret_cast<hipStream_t>(stream));
+}
+
+extern "C" snack_status snack_qk_rope_bwd_work(int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                                               int64_t* bytes)
+{
+    Heads q, k;
+    if (!bytes) return SNACK_ERR_INVALID_ARG;
+    SNACK_CHECK(make_heads(nullptr, 0, 0, q_heads, tokens, head_dim, SNACK_F32, &q));
+    SNACK_CHECK(make_heads(nullptr, 0, 0, k_heads, tokens, head_dim, SNACK_F32, &k));
+    uint32_t gq, gk, rq, rk;
+    bwd_splits(q.rows, k.rows, head_dim, &gq, &rq, &gk, &rk);
+    *bytes = ((int64_t)gq + gk) * head_dim * 4;
+    return SNACK_OK;
+}
+
+extern "C" snack_status snack_qk_rope_bwd(const void* Q, int64_t q_row, int64_t q_head, int32_t q_heads, const void* K,
+                                          int64_t k_row, int64_t k_head, int32_t k_heads, int32_t x_fmt,
+                                          int64_t tokens, int32_t head_dim, const int32_t* pos, const snack_rope* rope,
+                                          const float* q_gain, const float* k_gain, float eps, const void* dYq,
+                                          int64_t dq_row, int64_t dq_head, const void* dYk, int64_t dk_row,
+                                          int64_t dk_head, int32_t y_fmt, void* dXq, void* dXk, float* dq_gain,
+                                          float* dk_gain, void* work, int64_t work_bytes, snack_stream stream)
+{
+    BwdPart q{}, k{};
+    Rotation ro;
+    SNACK_CHECK(make_heads(q_gain ? Q : nullptr, q_row, q_head, q_heads, tokens, head_dim, x_fmt, &q.x));
+    SNACK_CHECK(make_heads(k_gain ? K : nullptr, k_row, k_head, k_heads, tokens, head_dim, x_fmt, &k.x));
+    SNACK_CHECK(make_heads(dYq, dq_row, dq_head, q_heads, tokens, head_dim, y_fmt, &q.g));
+    SNACK_CHECK(make_heads(dYk, dk_row, dk_head, k_heads, tokens, head_dim, y_fmt, &k.g));
+    SNACK_CHECK(make_rotation(rope, head_dim, pos, tokens, &ro));
+    if (!(eps >= 0) || !isfinite(eps) || (dq_gain && !q_gain) || (dk_gain && !k_gain)) return SNACK_ERR_INVALID_ARG;
+    const uintptr_t xa = x_fmt == SNACK_F32 ? 4 : 2;
+    if ((q.x.rows && (!dYq || !dXq || misaligned(dXq, xa) || (q_gain && !Q))) ||
+        (k.x.rows && (!dYk || !dXk || misaligned(dXk, xa) || (k_gain && !K))) || misaligned(q_gain, 4) ||
+        misaligned(k_gain, 4) || misaligned(dq_gain, 4) || misaligned(dk_gain, 4) || q_heads + (int64_t)k_heads == 0)
+        return SNACK_ERR_INVALID_ARG;
+    bwd_splits(q.x.rows, k.x.rows, head_dim, &q.groups, &q.run, &k.groups, &k.run);
+    if (dq_gain || dk_gain) {
+        const int64_t need = ((int64_t)q.groups + k.groups) * head_dim * 4;
+        if (need && (!work || misaligned(work, 4))) return SNACK_ERR_INVALID_ARG;
+        if (work_bytes < need) return SNACK_ERR_WORKSPACE;
+        if (dq_gain) q.part = (float*)work;
+        if (dk_gain) k.part = (float*)work + (int64_t)q.groups * head_dim;
+    }
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    ProfScope prof(KC_ROPE, s);
+    q.gain = q_gain;
+    k.gain = k_gain;
+    q.dx = dXq;
+    k.dx = dXk;
+    const unsigned groups = q.groups + k.groups;
+    if (groups) {
+        auto launch = [&](auto lanes, auto x, auto y) {
+            hipLaunchKernelGGL((qk_bwd_kernel<decltype(lanes)::value, decltype(x), decltype(y)>), dim3(groups),
+                               dim3(kThreads), 0, s, q, k, head_dim, pos, ro, (double)eps, 1.0 / head_dim);
+        };
+        auto types = [&](auto lanes) {
+            if (x_fmt == SNACK_F32) {
+                if (y_fmt == SNACK_F32) launch(lanes, float{}, float{});
+                else launch(lanes, float{}, uint16_t{});
+            } else {
+                if (y_fmt == SNACK_F32) launch(lanes, uint16_t{}, float{});
+                else launch(lanes, uint16_t{}, uint16_t{});
+            }
+        };
+        switch (head_lanes(head_dim)) {
+        case 4: types(std::integral_constant<int, 4>{}); break;
+        case 8: types(std::integral_constant<int, 8>{}); break;
+        case 16: types(std::integral_constant<int, 16>{}); break;
+        default: types(std::integral_constant<int, 32>{}); break;
+        }
+        SNACK_HIP(hipGetLastError());
+    }
+    if (dq_gain || dk_gain) {
+        hipLaunchKernelGGL(gain_sum_kernel, dim3((unsigned)(head_dim + 31) / 32, 2), dim3(kSumThreads), 0, s, q.part,
+                           q.groups, dq_gain, k.part, k.groups, dk_gain, head_dim);
+        SNACK_HIP(hipGetLastError());
+    }
+    return SNACK_OK;
+}

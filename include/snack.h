@@ -427,6 +427,178 @@ snack_status snack_backward_ckpt(snack_layer* layer, const uint8_t* Q, const uin
                                  float* dX, float* dW, int32_t B, snack_stream stream);
 
 /*
+ * The attention half of a transformer block: the norms and the rotary positions of
+ * its queries and keys, a cache that keeps keys and values in 8 or 4 bits, and the
+ * attention over that cache.
+ *
+ * Heads: an argument named X, x_row, x_head is a device array of [tokens, heads,
+ * head_dim] in which token t's head h starts at X + t x_row + h x_head (in
+ * elements; the head_dim features lie side by side), so that the parts of one
+ * projection's output rows are taken as they lie.  Outputs are contiguous.  1 <=
+ * head_dim <= 256.  x_fmt, y_fmt: SNACK_F32 or SNACK_BF16.
+ *
+ * These calls allocate nothing, never synchronise and use no atomics (repeated
+ * calls give the same bits), and may be captured in a HIP graph: they read every
+ * device array when the graph runs.  tokens = 0 is allowed and does nothing (gain
+ * gradients are then 0).  tokens x heads below 2^31, else SNACK_ERR_UNSUPPORTED.
+ * No output may overlap an input.
+ */
+#define SNACK_E2M1 4   /* 4-bit e2m1 numbers (of a cache only) */
+
+#define SNACK_ROPE_HALF 0    /* feature i turns with feature i + rot / 2 */
+#define SNACK_ROPE_PAIRS 1   /* feature 2 i turns with feature 2 i + 1 */
+
+/*
+ * Rotary positions.  table: device float[positions, rot]: for every position the
+ * cosines of rot / 2 angles, then their sines.  The first rot features of a head
+ * are rotated (rot even, at most head_dim), the others left as they are.  A
+ * position outside the table makes its token's rows NaN.
+ */
+typedef struct snack_rope {
+    const float* table;
+    int32_t positions;
+    int32_t rot;
+    int32_t layout;     /* SNACK_ROPE_HALF or SNACK_ROPE_PAIRS */
+} snack_rope;
+
+/*
+ * The table: cos and sin of p f_i, each times amplitude, computed in 64 bits and
+ * rounded once; f_i = base^(-2 i / rot).  For contexts longer than the one trained
+ * on: with trained = 0 every f_i is divided by factor; with trained > 0 (tokens)
+ * pair i, which makes r_i = trained f_i / 2 pi turns in it, gets
+ * f_i (w + (1 - w) / factor), w = (r_i - low) / (high - low) within [0, 1].
+ * base > 0, factor > 0, low < high, all finite.
+ */
+snack_status snack_rope_table(int32_t positions, int32_t rot, double base, double factor, double trained, double low,
+                              double high, double amplitude, float* table, snack_stream stream);
+
+/*
+ * Norms of queries and keys for each head, and their rotation, in one pass:
+ *   y = x / sqrt(mean over the head of x^2 + eps) gain,   then the rotation of y.
+ * Computed in 64 bits, rounded to fp32 once (and from there to bf16).
+ *   Q, K          the queries and keys (K NULL with k_heads = 0: none).
+ *   pos           device int32[tokens]; unused (may be NULL) without a rotation.
+ *   rope          NULL: no rotation.
+ *   q_gain, k_gain  device float[head_dim]; NULL: those heads are not normed.
+ *   Yq, Yk        [tokens, q_heads, head_dim], [tokens, k_heads, head_dim] in y_fmt.
+ */
+snack_status snack_qk_rope_fwd(const void* Q, int64_t q_row, int64_t q_head, int32_t q_heads, const void* K,
+                               int64_t k_row, int64_t k_head, int32_t k_heads, int32_t x_fmt, int64_t tokens,
+                               int32_t head_dim, const int32_t* pos, const snack_rope* rope, const float* q_gain,
+                               const float* k_gain, float eps, void* Yq, void* Yk, int32_t y_fmt, snack_stream stream);
+/*
+ * Its gradient, from those of Yq and Yk (dYq, dYk in y_fmt, laid out as heads).
+ * With dy the gradient turned back, xh = x rstd, w = dy gain:
+ *   dx = rstd (w - xh mean(w xh)),   dgain = sum over tokens and heads of dy xh
+ * (without a gain dx = dy, and x is not read: Q and K may be NULL there).
+ *   dXq, dXk  contiguous, in x_fmt;  dq_gain, dk_gain  device float[head_dim],
+ *             NULL: not wanted (they must be where there is no gain).
+ *   work      device scratch of snack_qk_rope_bwd_work bytes, used within the call
+ *             (SNACK_ERR_WORKSPACE when work_bytes is less); may be NULL where
+ *             neither gain gradient is wanted.
+ */
+snack_status snack_qk_rope_bwd_work(int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t head_dim,
+                                    int64_t* bytes);
+snack_status snack_qk_rope_bwd(const void* Q, int64_t q_row, int64_t q_head, int32_t q_heads, const void* K,
+                               int64_t k_row, int64_t k_head, int32_t k_heads, int32_t x_fmt, int64_t tokens,
+                               int32_t head_dim, const int32_t* pos, const snack_rope* rope, const float* q_gain,
+                               const float* k_gain, float eps, const void* dYq, int64_t dq_row, int64_t dq_head,
+                               const void* dYk, int64_t dk_row, int64_t dk_head, int32_t y_fmt, void* dXq, void* dXk,
+                               float* dq_gain, float* dk_gain, void* work, int64_t work_bytes, snack_stream stream);
+
+/*
+ * A cache of keys and values: pages of page_tokens tokens (a multiple of 32) for
+ * `heads` heads of head_dim features, in blocks of 32 features as a checkpoint's
+ * (fmt SNACK_INT8, SNACK_E4M3 or SNACK_E2M1: codes of at most 127, 448 or 6 in
+ * magnitude, and the same exponent byte; a block that holds a NaN or an infinity
+ * reads back as NaN).  data: snack_cache_bytes bytes of device memory, 16-byte
+ * aligned; how it lies in them is the library's own.  Memory that no token was
+ * written to may hold anything.  A token's place is its slot: page * page_tokens +
+ * offset in the page.  pages * page_tokens below 2^36, heads below
+ * 2^13, heads * page_tokens below 2^31.
+ *
+ * Which pages are a sequence's says a page table: device int32[sequences, width],
+ * the pages of its tokens 0, page_tokens, 2 page_tokens, ...; entries past its
+ * length are not read.  Sequences may share pages that none of them writes.
+ *
+ * A call's tokens are those of the sequences one after the other, the newest of
+ * each: sequence b has tokens starts[b] .. starts[b + 1] - 1 (device
+ * int32[sequences + 1], ascending; NULL: tokens / sequences each, which must then
+ * divide), the last of the lens[b] (device int32[sequences]) that the cache holds
+ * of it with them.  Tokens outside of starts belong to no sequence.
+ */
+typedef struct snack_cache {
+    uint8_t* data;
+    int64_t pages;
+    int32_t page_tokens;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t fmt;
+} snack_cache;
+
+/* The size of a cache's data (its data pointer is not read). */
+snack_status snack_cache_bytes(const snack_cache* cache, int64_t* bytes);
+
+/*
+ * Positions (pos, device int32[tokens]) and slots (device int64[tokens]) of a
+ * call's tokens, the same for every block of a model.  A token of no sequence, or
+ * whose page the table does not name (past its width, or no page of the cache),
+ * gets slot -1, and position 0 where it has none.
+ */
+snack_status snack_cache_slots(const snack_cache* cache, const int32_t* table, int32_t width, const int32_t* lens,
+                               const int32_t* starts, int32_t sequences, int64_t tokens, int32_t* pos, int64_t* slot,
+                               snack_stream stream);
+
+/*
+ * Keep keys and values: K, V heads of x_fmt, slot device int64[tokens].  A slot
+ * outside the cache is not written; the slots of one call are distinct.  Values are
+ * rounded once, nearest even.
+ */
+snack_status snack_cache_write(const snack_cache* cache, const void* K, int64_t k_row, int64_t k_head, const void* V,
+                               int64_t v_row, int64_t v_head, int32_t x_fmt, int64_t tokens, const int64_t* slot,
+                               snack_stream stream);
+/*
+ * snack_qk_rope_fwd whose keys go into the cache (rounded to fp32, then as
+ * snack_cache_write), the values with them, in one launch.
+ */
+snack_status snack_cache_write_rope(const snack_cache* cache, const void* Q, int64_t q_row, int64_t q_head,
+                                    int32_t q_heads, const void* K, int64_t k_row, int64_t k_head, const void* V,
+                                    int64_t v_row, int64_t v_head, int32_t x_fmt, int64_t tokens, const int32_t* pos,
+                                    const int64_t* slot, const snack_rope* rope, const float* q_gain,
+                                    const float* k_gain, float eps, void* Yq, int32_t y_fmt, snack_stream stream);
+/*
+ * The values that the cache stands for at device int64 slot[tokens]: K and V
+ * (either may be NULL) [tokens, heads, head_dim] as SNACK_F32 (exact) or SNACK_BF16
+ * (exact down to steps of 2^-133).  A negative slot gives zeros, one past the cache NaN.
+ */
+snack_status snack_cache_read(const snack_cache* cache, const int64_t* slot, int64_t tokens, void* K, void* V,
+                              int32_t y_fmt, snack_stream stream);
+
+/*
+ * Attention of a call's tokens over the cache.  Q: heads of q_fmt (q_heads a
+ * multiple of cache.heads; query head h reads cache head h / (q_heads /
+ * cache.heads)); out [tokens, q_heads, head_dim] in q_fmt:
+ *   s_t = scale q . k_t,   out = sum_t softmax(s)_t v_t
+ * over the tokens t < lens[b] of its sequence, with `causal` only those up to its
+ * own (t <= lens[b] - its sequence's tokens in this call + its index among them).
+ * A query that sees no token gets 0; tokens of no sequence are not written.  What a
+ * query does not see has no influence on it, whatever it holds (NaN too).  A query
+ * that would read past the table's width or a page the cache does not have gets NaN.
+ * scale finite, above 0.  Sums, maxima and the softmax are held in fp32.
+ * SNACK_F32: q and the softmax's terms enter the products exactly, as sums of three
+ * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are rounded to bf16
+ * (at most 16 queries a head: to two).
+ *   work  device scratch of snack_cache_attend_work bytes, 16-byte aligned, used
+ *         within the call (SNACK_ERR_WORKSPACE when work_bytes is less).
+ */
+snack_status snack_cache_attend_work(const snack_cache* cache, int32_t q_heads, int64_t tokens, int32_t sequences,
+                                     int64_t* bytes);
+snack_status snack_cache_attend(const snack_cache* cache, const void* Q, int64_t q_row, int64_t q_head,
+                                int32_t q_heads, int32_t q_fmt, int64_t tokens, const int32_t* table, int32_t width,
+                                const int32_t* lens, const int32_t* starts, int32_t sequences, float scale,
+                                int32_t causal, void* out, void* work, int64_t work_bytes, snack_stream stream);
+
+/*
  * Kernel timing.  While enabled, the library brackets each of its kernel
  * launches with HIP events recorded on the launch stream; snack_profile_read
  * synchronises those events and returns, for one kernel class, the launch count
