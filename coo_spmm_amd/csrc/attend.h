@@ -49,20 +49,19 @@ struct AttendArgs {
     FastDiv by_group;                 // query heads of a cache head
     float scale_log2;                 // scale * log2(e)
     int32_t causal;
-    float* part;                      // two partial results a workgroup: of the unit it goes on with, of the one it starts
-    int4* meta;                       // of the unit a workgroup starts and does not end: sequence, unit in it, pieces
+    float* part;                      // two partial results a workgroup: of the block it goes on with, of the one it starts
+    int4* meta;                       // of the block a workgroup starts and does not end: sequence, block, head, pieces
 };
 
-// floats of a partial result: the output's, then maximum and sum of every query
+// floats of a partial result of 16 queries: the output's, then maximum and sum of every query
 __host__ __device__ constexpr int part_floats(int nb) { return 2 * nb * 256 + 2 * kQueries; }
 
 // a sequence of the call
 struct Seq {
     int32_t first, nq, len;
-    int32_t blocks;   // of kQueries queries of a cache head
     int32_t tiles;    // at least 1 (a query that sees nothing is still answered)
 };
-__device__ inline Seq get_seq(const AttendArgs& a, int32_t b, int rows)
+__device__ inline Seq get_seq(const AttendArgs& a, int32_t b)
 {
     Seq s;
     int32_t last;
@@ -75,12 +74,168 @@ __device__ inline Seq get_seq(const AttendArgs& a, int32_t b, int rows)
     }
     s.nq = last - s.first;
     s.len = max(a.lens[b], 0);
-    s.blocks = (int32_t)(((int64_t)s.nq * a.by_group.d + rows - 1) / rows);
     // tokens past the page table are one more tile, which stands for all of them
     const int64_t room = (int64_t)a.width * a.c.page_tiles + 1;
     const int64_t t = ((int64_t)s.len + kTile - 1) / kTile;
     s.tiles = (int32_t)(t < 1 ? 1 : t < room ? t : room);
     return s;
+}
+
+// The queries of a cache head in a sequence (its tokens times the query heads of the group) are cut into blocks of
+// ROWS.  A block takes its tiles up to the last one that its last query sees.
+template <int ROWS>
+__device__ inline int32_t seq_blocks(const AttendArgs& a, const Seq& s)
+{
+    return (int32_t)(((uint32_t)s.nq * a.by_group.d + ROWS - 1) / ROWS);
+}
+template <int ROWS>
+__device__ inline int32_t block_tiles(const AttendArgs& a, const Seq& s, int32_t k)
+{
+    if (!a.causal) return s.tiles;
+    const uint32_t rows = (uint32_t)s.nq * a.by_group.d, last = min((uint32_t)(k + 1) * ROWS, rows) - 1;
+    const int64_t seen = (int64_t)s.len - s.nq + fast_quot(a.by_group, last) + 1;
+    const int64_t t = (seen + kTile - 1) >> 5;
+    return (int32_t)(t < 1 ? 1 : t < s.tiles ? t : s.tiles);
+}
+
+// The work: for every sequence, every block of queries, every cache head, the block's tiles, all one after the other.
+// Where a position of this row lies:
+struct Cursor {
+    int32_t b, k;             // sequence, block
+    int32_t blocks, tiles;    // of the sequence, of the block (of every head of it)
+    Seq s;
+};
+template <int ROWS>
+__device__ inline void set_cursor(const AttendArgs& a, Cursor& c, int32_t b, int32_t k)
+{
+    c.b = b;
+    c.k = k;
+    c.s = get_seq(a, b);
+    c.blocks = seq_blocks<ROWS>(a, c.s);
+}
+// the next block; past the last sequence c.b is the number of sequences
+template <int ROWS>
+__device__ inline void next_block(const AttendArgs& a, Cursor& c)
+{
+    ++c.k;
+    while (c.k >= c.blocks) {
+        if (c.b + 1 >= a.sequences) {
+            c.b = a.sequences;
+            return;
+        }
+        set_cursor<ROWS>(a, c, c.b + 1, 0);
+    }
+    c.tiles = block_tiles<ROWS>(a, c.s, c.k);
+}
+
+// x's sum over the threads before this one; lds holds THREADS / 64 numbers more than it takes, of which the first
+// THREADS get the sums
+template <int THREADS, typename T>
+__device__ inline T group_scan(T x, T* lds, T* total)
+{
+    const int lane = (int)threadIdx.x & (kWave - 1), wave = (int)threadIdx.x / kWave;
+    T y = x;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const T z = __shfl_up(y, d, kWave);
+        if (lane >= d) y += z;
+    }
+    if (lane == kWave - 1) lds[THREADS + wave] = y;
+    __syncthreads();
+    T sum = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / kWave; ++i) {
+        if (i == wave) y += sum;
+        sum += lds[THREADS + i];
+    }
+    lds[threadIdx.x] = y - x;
+    __syncthreads();
+    *total = sum;
+    return y - x;
+}
+// the last of n ascending numbers that is at most x (the first is)
+template <int N, typename T>
+__device__ inline int last_at_most(const T* v, T x)
+{
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (v[m] <= x) lo = m;
+        else hi = m - 1;
+    }
+    return lo;
+}
+
+// The workgroup's threads take a run of sequences each to count the blocks, then a run of blocks each to count the
+// tiles.
+template <int THREADS>
+struct Schedule {
+    int32_t seqs[THREADS + THREADS / kWave];   // blocks before a thread's run of sequences
+    int64_t work[THREADS + THREADS / kWave];   // tiles before a thread's run of blocks
+};
+template <int THREADS, int ROWS>
+__device__ inline Cursor find_block(const AttendArgs& a, const Schedule<THREADS>& l, int32_t i)
+{
+    Cursor c;
+    if (!a.starts) {
+        const int32_t blocks = (int32_t)(((uint32_t)a.per * a.by_group.d + ROWS - 1) / ROWS);
+        set_cursor<ROWS>(a, c, i / blocks, i % blocks);
+    } else {
+        const int th = last_at_most<THREADS>(l.seqs, i);
+        const int32_t run = (a.sequences + THREADS - 1) / THREADS;
+        set_cursor<ROWS>(a, c, th * run, 0);
+        c.k = i - l.seqs[th];
+        while (c.k >= c.blocks) {
+            const int32_t k = c.k - c.blocks;
+            set_cursor<ROWS>(a, c, c.b + 1, k);
+        }
+    }
+    c.tiles = block_tiles<ROWS>(a, c.s, c.k);
+    return c;
+}
+// all tiles, and the runs' sums in l
+template <int THREADS, int ROWS>
+__device__ inline int64_t count_work(const AttendArgs& a, Schedule<THREADS>& l, int32_t* all_blocks)
+{
+    int32_t blocks = 0;
+    if (!a.starts) {
+        blocks = a.sequences * (int32_t)(((uint32_t)a.per * a.by_group.d + ROWS - 1) / ROWS);
+    } else {
+        const int32_t run = (a.sequences + THREADS - 1) / THREADS;
+        const int32_t b0 = min((int32_t)threadIdx.x * run, a.sequences), b1 = min(b0 + run, a.sequences);
+        int32_t n = 0;
+        for (int32_t b = b0; b < b1; ++b) n += seq_blocks<ROWS>(a, get_seq(a, b));
+        group_scan<THREADS>(n, l.seqs, &blocks);
+    }
+    *all_blocks = blocks;
+    const int32_t run = (blocks + THREADS - 1) / THREADS;
+    const int32_t i0 = min((int32_t)threadIdx.x * run, blocks), i1 = min(i0 + run, blocks);
+    int64_t w = 0, total;
+    if (i0 < i1) {
+        Cursor c = find_block<THREADS, ROWS>(a, l, i0);
+        for (int32_t i = i0; i < i1; ++i) {
+            w += c.tiles;
+            next_block<ROWS>(a, c);
+        }
+    }
+    group_scan<THREADS>(w * a.c.heads, l.work, &total);
+    return total;
+}
+// the block that has tile `pos` of them all; before: the tiles before that block
+template <int THREADS, int ROWS>
+__device__ inline Cursor find_work(const AttendArgs& a, const Schedule<THREADS>& l, int32_t all_blocks, int64_t pos,
+                                   int64_t* before)
+{
+    const int th = last_at_most<THREADS>(l.work, pos);
+    const int32_t run = (all_blocks + THREADS - 1) / THREADS;
+    Cursor c = find_block<THREADS, ROWS>(a, l, th * run);
+    int64_t at = l.work[th];
+    while (pos >= at + (int64_t)c.tiles * a.c.heads) {
+        at += (int64_t)c.tiles * a.c.heads;
+        next_block<ROWS>(a, c);
+    }
+    *before = at;
+    return c;
 }
 
 // the largest, or the sum, of x over the four lanes of a query (16 apart)
@@ -283,86 +438,47 @@ __device__ inline void unroll(F f)
 // the first n of 8 tokens' bytes of a word pair kept, n within 0..8
 __device__ inline uint64_t first_bytes(int n) { return n >= 8 ? ~0ull : n <= 0 ? 0ull : (1ull << (8 * n)) - 1; }
 
-// The codes and exponents of the tokens past the first n of the lane's eight become 0.
-template <int FMT, int NB>
-__device__ inline void clear_values(RawTile<FMT, NB>& r, int n)
+// A V block's codes and exponents of the tokens whose byte is not in m become 0.
+template <int FMT>
+__device__ inline void clear_block(uint32_t* v, uint32_t* ve, uint64_t m)
 {
-    const uint64_t m = first_bytes(n);
     const uint32_t m0 = (uint32_t)m, m1 = (uint32_t)(m >> 32);
+    ve[0] &= m0;
+    ve[1] &= m1;
+    if constexpr (four_bits(FMT)) {
+        v[0] &= m0;
+        v[1] &= m1;
+    } else {
+        // two bytes a token
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        r.ve[2 * b] &= m0;
-        r.ve[2 * b + 1] &= m1;
-        if constexpr (four_bits(FMT)) {
-            r.v[2 * b] &= m0;
-            r.v[2 * b + 1] &= m1;
-        } else {
-            // two bytes a token
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t x = (i < 2 ? m0 : m1) >> (16 * (i & 1));
-                r.v[4 * b + i] &= (x & 0xFFu ? 0xFFFFu : 0u) | (x & 0xFF00u ? 0xFFFF0000u : 0u);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = (i < 2 ? m0 : m1) >> (16 * (i & 1));
+            v[i] &= (x & 0xFFu ? 0xFFFFu : 0u) | (x & 0xFF00u ? 0xFFFF0000u : 0u);
         }
     }
 }
-
-// Where position `pos` of the row of tiles lies: the sequence and the tiles of it before. The workgroup's threads
-// take a run of sequences each; total: all tiles.
-struct Spot {
-    int32_t b;
-    int64_t before;
-};
-template <int THREADS>
-__device__ inline int64_t total_work(const AttendArgs& a, int rows, int64_t* sums)
+// The tokens of the tile (a bit each, the same in every lane) whose exponent byte in this V block is 255, which
+// becomes 0 (their codes are 0).
+__device__ inline uint32_t take_nans(uint32_t* ve)
 {
-    const int32_t run = (a.sequences + THREADS - 1) / THREADS;
-    const int32_t b0 = min((int32_t)threadIdx.x * run, a.sequences), b1 = min(b0 + run, a.sequences);
-    int64_t w = 0;
-    for (int32_t b = b0; b < b1; ++b) {
-        const Seq s = get_seq(a, b, rows);
-        w += (int64_t)a.c.heads * s.blocks * s.tiles;
-    }
-    // inclusive sums over the threads
-    int64_t x = w;
+    uint32_t any = 0;
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int64_t y = __shfl_up(x, d, kWave);
-        if (((int)threadIdx.x & (kWave - 1)) >= d) x += y;
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = ~ve[i];
+        any |= (x - 0x01010101u) & ~x & 0x80808080u;
     }
-    const int wave = (int)threadIdx.x / kWave;
-    if (((int)threadIdx.x & (kWave - 1)) == kWave - 1) sums[THREADS + wave] = x;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int i = 0; i < THREADS / kWave; ++i) {
-        if (i == wave) x += total;
-        total += sums[THREADS + i];
+    if (__ballot(any != 0) == 0) return 0;
+    uint64_t e = (uint64_t)ve[1] << 32 | ve[0];
+    uint32_t tokens = 0;
+    for (int j = 0; j < 8; ++j) {
+        const bool is = (e >> (8 * j) & 0xFFu) == 255u;
+        if (is) e &= ~(0xFFull << (8 * j));
+        const uint64_t m = __ballot(is);
+        for (int g = 0; g < 4; ++g) tokens |= (uint32_t)(m >> (16 * g) & 1) << (8 * g + j);
     }
-    sums[threadIdx.x] = x - w;   // before this thread's run
-    __syncthreads();
-    return total;
-}
-template <int THREADS>
-__device__ inline Spot find_spot(const AttendArgs& a, int rows, const int64_t* sums, int64_t pos)
-{
-    // the last thread whose run starts at or before pos, then the sequences of its run (the runs past the last
-    // sequence are empty and start at the total, which is past pos)
-    int lo = 0, hi = THREADS - 1;
-    while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (sums[m] <= pos) lo = m;
-        else hi = m - 1;
-    }
-    const int32_t run = (a.sequences + THREADS - 1) / THREADS;
-    Spot at{lo * run, sums[lo]};
-    for (;;) {
-        const Seq s = get_seq(a, at.b, rows);
-        const int64_t w = (int64_t)a.c.heads * s.blocks * s.tiles;
-        if (pos < at.before + w || at.b + 1 >= a.sequences) return at;
-        at.before += w;
-        ++at.b;
-    }
+    ve[0] = (uint32_t)e;
+    ve[1] = (uint32_t)(e >> 32);
+    return tokens;
 }
 
 // one query's row of the output: token and query head of query `row` of cache head h
@@ -401,248 +517,26 @@ __device__ inline void store_out(void* out, int64_t at, int d, int dims, f32x4 v
     }
 }
 
-// Values of a tile in which some query does not see some token: what has the exponent byte 255 is NaN, and a query
-// that gives it the weight 0 because it does not see it must not get 0 NaN.  Their exponents become 0 (codes are 0),
-// and the queries that do see them get their NaN here.
-template <int FMT, int NB>
-__device__ inline void nan_values(RawTile<FMT, NB>& r, f32x4* o, int64_t base, int64_t limit)
-{
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < 2 * NB; ++i) {
-        const uint32_t x = ~r.ve[i];
-        any |= (x - 0x01010101u) & ~x & 0x80808080u;
-    }
-    if (__ballot(any != 0) == 0) return;
-    unroll<NB>([&](auto bc) {
-        constexpr int b = decltype(bc)::value;
-        const uint64_t e = (uint64_t)r.ve[2 * b + 1] << 32 | r.ve[2 * b];
-        uint64_t kept = e;
-        for (int j = 0; j < 8; ++j) {
-            const bool is = (e >> (8 * j) & 0xFFu) == 255u;
-            if (is) kept &= ~(0xFFull << (8 * j));
-            const uint64_t m = __ballot(is);
-            for (int g = 0; g < 4; ++g)
-                if ((m >> (16 * g) & 1) && base + 8 * g + j <= limit) {
-                    const float nan = __builtin_nanf("");
-                    o[2 * b] = o[2 * b + 1] = f32x4{nan, nan, nan, nan};
-                }
-        }
-        r.ve[2 * b] = (uint32_t)kept;
-        r.ve[2 * b + 1] = (uint32_t)(kept >> 32);
-    });
-}
-
-template <int FMT, int NB, int QT>
-__global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel(AttendArgs a)
-{
-    constexpr int QP = QT == SNACK_F32 ? 3 : 1, PP = QT == SNACK_F32 ? 3 : 2;
-    using Q = typename QType<QT>::T;
-    __shared__ int64_t sums[kAttendThreads + kAttendWaves];
-    __shared__ f32x4 so[kAttendWaves][2 * NB][kWave];
-    __shared__ float2 sml[kAttendWaves][kQueries];
-    const int lane = (int)threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    const int col = lane & 15, g = lane >> 4;
-
-    const int64_t total = total_work<kAttendThreads>(a, kQueries, sums);
-    int64_t run = (total + gridDim.x - 1) / gridDim.x;
-    if (run < kMinRun) run = kMinRun;
-    int64_t pos = run * blockIdx.x;
-    const int64_t end = min(total, pos + run);
-    if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
-    if (pos >= end) return;
-    const Spot spot = find_spot<kAttendThreads>(a, kQueries, sums, pos);
-    int32_t b = __builtin_amdgcn_readfirstlane(spot.b);
-    Seq s = get_seq(a, b, kQueries);
-    int64_t within = pos - spot.before;   // tiles of the sequence's units before pos
-    int32_t unit = (int32_t)(within / s.tiles);
-    int32_t t0 = (int32_t)(within - (int64_t)unit * s.tiles);
-
-    while (pos < end) {
-        // sequences without a query have no unit
-        while (unit >= a.c.heads * s.blocks) {
-            unit = 0;
-            s = get_seq(a, ++b, kQueries);
-        }
-        const int32_t h = unit / s.blocks, block = unit - h * s.blocks;
-        const int32_t t1 = (int32_t)min((int64_t)s.tiles, t0 + (end - pos));
-        const uint32_t rows = (uint32_t)s.nq * a.by_group.d, row0 = (uint32_t)block * kQueries;
-        const uint32_t row = row0 + col;
-        const bool live = row < rows;
-        const Row mine = get_row(a, h, live ? row : rows - 1);
-        // the last token a query sees, of this lane's and of the unit's first
-        const int64_t past = a.causal ? (int64_t)s.len - s.nq : (int64_t)s.len - 1;
-        const int64_t limit = a.causal ? past + mine.i : past;
-        const int64_t least = a.causal ? past + fast_quot(a.by_group, row0) : past;
-
-        bf16x8 q[QP][NB];
-        {
-            const Q* p = (const Q*)a.q + (int64_t)(s.first + mine.i) * a.q_row + (int64_t)mine.head * a.q_head + 8 * g;
-            unroll<NB>([&](auto jc) {
-                constexpr int j = decltype(jc)::value;
-                const f32x8 x = load8(p + 32 * j, a.c.d - 8 * g - 32 * j);
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = x[i];
-                bf16x8 part[QP];
-                split8<QP>(y, part);
-#pragma unroll
-                for (int k = 0; k < QP; ++k) q[k][j] = part[k];
-            });
-        }
-
-        f32x4 o[2 * NB];
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) o[i] = f32x4{0, 0, 0, 0};
-        float mc = -__builtin_inff(), l = 0.0f;   // running maximum times scale_log2; this lane's sum
-
-        const int32_t* pages = a.table + (int64_t)b * a.width;
-        auto page_of = [&](int32_t t) {
-            const int32_t p = (int32_t)fast_quot(a.c.by_page, (uint32_t)t);
-            return p < a.width ? pages[p] : -1;
-        };
-        auto tile_at = [&](int32_t t, int32_t page) {
-            const uint32_t p = fast_quot(a.c.by_page, (uint32_t)t);
-            const bool ok = page >= 0 && page < a.pages;
-            return a.c.data + (int64_t)(ok ? page : 0) * a.c.page_bytes +
-                   ((int64_t)h * a.c.page_tiles + (t - p * a.c.page_tiles)) * a.c.record;
-        };
-        RawTile<FMT, NB> cur, next;
-        int32_t t = t0 + wave;
-        int32_t page = 0, page1 = 0;
-        if (t < t1) {
-            page = page_of(t);
-            page1 = page_of(min(t + kAttendWaves, t1 - 1));
-            load_tile(cur, tile_at(t, page), lane);
-        }
-        for (; t < t1; t += kAttendWaves) {
-            const int32_t tn = min(t + kAttendWaves, t1 - 1);
-            load_tile(next, tile_at(tn, page1), lane);
-            const int32_t page2 = page_of(min(t + 2 * kAttendWaves, t1 - 1));
-            const int64_t base = (int64_t)t * kTile;
-            const bool bad = page < 0 || page >= a.pages;
-            f32x4 sc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-            unroll<NB>([&](auto jc) {
-                constexpr int j = decltype(jc)::value;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const bf16x8 k = key_operand<FMT, NB, j>(cur.k[half], cur.ke[half]);
-#pragma unroll
-                    for (int i = QP - 1; i >= 0; --i)
-                        sc[half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[i][j], sc[half], 0, 0, 0);
-                }
-            });
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = sc[i >> 2][i & 3];
-            if (bad || base + kTile - 1 > least) {
-                if (bad) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = __builtin_nanf("");
-                    clear_values(cur, 0);
-                } else {
-                    const int64_t left = (int64_t)s.len - base - 8 * g;
-                    clear_values(cur, left > 8 ? 8 : left < 0 ? 0 : (int)left);
-                    if (a.causal) nan_values(cur, o, base, live ? limit : -1);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (base + 8 * g + i > limit) x[i] = -__builtin_inff();
-            }
-            const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                                    fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * a.scale_log2;
-            if (__ballot(top > mc + kRaise)) {
-                const float m = fmaxf(mc, query_max(top));
-                const float f = m == mc ? 1.0f : __builtin_amdgcn_exp2f(mc - m);
-#pragma unroll
-                for (int i = 0; i < 2 * NB; ++i) o[i] *= f;
-                l *= f;
-                mc = m;
-            }
-            const float off = mc == -__builtin_inff() ? 0.0f : -mc;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], a.scale_log2, off));
-                l += x[i];
-            }
-            bf16x8 p[PP];
-            split8<PP>(x, p);
-            unroll<NB>([&](auto bc) {
-                constexpr int blk = decltype(bc)::value;
-                bf16x8 lo, hi;
-                value_operands<FMT, NB, blk>(cur.v, cur.ve, lo, hi);
-#pragma unroll
-                for (int i = PP - 1; i >= 0; --i) {
-                    o[2 * blk] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, p[i], o[2 * blk], 0, 0, 0);
-                    o[2 * blk + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, p[i], o[2 * blk + 1], 0, 0, 0);
-                }
-            });
-            cur = next;
-            page = page1;
-            page1 = page2;
-        }
-        // the wavefronts' results of the unit, joined
-        l = query_sum(l);
-        if (g == 0) sml[wave][col] = make_float2(mc, l);
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) so[wave][i][lane] = o[i];
-        __syncthreads();
-        float m = -__builtin_inff();
-#pragma unroll
-        for (int w = 0; w < kAttendWaves; ++w) m = fmaxf(m, sml[w][col].x);
-        const float ms = m == -__builtin_inff() ? 0.0f : m;
-        float f[kAttendWaves], sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kAttendWaves; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(sml[w][col].x - ms);
-            sum = fmaf(f[w], sml[w][col].y, sum);
-        }
-        const bool whole = t0 == 0 && t1 == s.tiles;
-        float* part = a.part + (int64_t)(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * part_floats(NB);
-        const int64_t at = ((int64_t)(s.first + mine.i) * a.hq + mine.head) * a.c.d;
-        const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-        for (int i = wave; i < 2 * NB; i += kAttendWaves) {
-            f32x4 v = {0, 0, 0, 0};
-#pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w) v += so[w][i][lane] * f[w];
-            v *= inv;
-            if (!live) continue;
-            if (whole) store_out<QT>(a.out, at, 16 * i + 4 * g, a.c.d, v);
-            else *reinterpret_cast<f32x4*>(part + (i * kWave + lane) * 4) = v;
-        }
-        if (!whole && wave == 0 && g == 0)
-            *reinterpret_cast<float2*>(part + 2 * NB * 256 + 2 * col) = make_float2(m, sum);
-        if (!whole && t0 == 0 && threadIdx.x == 0) {
-            // pieces: this one and those of the workgroups up to the one that has the unit's last tile
-            const int64_t rest = s.tiles - t1;
-            a.meta[blockIdx.x] = make_int4(b, unit, (int32_t)(1 + (rest + run - 1) / run), 0);
-        }
-        __syncthreads();
-        pos += t1 - t0;
-        t0 = 0;
-        ++unit;
-    }
-}
-
-// The pieces of the unit that workgroup blockIdx.x of the first launch started, joined; 16 features (blockIdx.y).
-template <int QT>
+// The pieces of the unit that workgroup blockIdx.x of the first launch started, joined; 16 features (blockIdx.y) of 16
+// queries (blockIdx.z).
+template <int QT, int ROWS>
 __global__ void __launch_bounds__(kAttendThreads) attend_join_kernel(AttendArgs a)
 {
     __shared__ f32x4 so[kAttendWaves][kWave];
     __shared__ float2 sml[kAttendWaves][kQueries];
     const int4 u = a.meta[blockIdx.x];
-    if (u.z == 0) return;
+    if (u.w == 0) return;
     const int lane = (int)threadIdx.x & (kWave - 1), wave = (int)threadIdx.x / kWave;
     const int col = lane & 15, g = lane >> 4, i = (int)blockIdx.y;
     const int size = part_floats(a.c.nb);
-    const Seq s = get_seq(a, u.x, kQueries);
-    const int32_t h = u.y / s.blocks, block = u.y - h * s.blocks;
-    const uint32_t rows = (uint32_t)s.nq * a.by_group.d, row = (uint32_t)block * kQueries + col;
+    const Seq s = get_seq(a, u.x);
+    const int32_t h = u.z;
+    const uint32_t rows = (uint32_t)s.nq * a.by_group.d, row = (uint32_t)u.y * ROWS + 16 * blockIdx.z + col;
     const bool live = row < rows;
     float m = -__builtin_inff(), sum = 0.0f;
     f32x4 v = {0, 0, 0, 0};
-    for (int k = wave; k < u.z; k += kAttendWaves) {
-        const float* part = a.part + (int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * size;
+    for (int k = wave; k < u.w; k += kAttendWaves) {
+        const float* part = a.part + ((int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * (ROWS / 16) + blockIdx.z) * size;
         float2 ml = make_float2(-__builtin_inff(), 0.0f);
         f32x4 x = {0, 0, 0, 0};
         if (live) {
@@ -676,30 +570,14 @@ __global__ void __launch_bounds__(kAttendThreads) attend_join_kernel(AttendArgs 
     store_out<QT>(a.out, at, 16 * i + 4 * g, a.c.d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
 }
 
-template <int FMT>
-snack_status launch_attend(const AttendArgs& a, int q_fmt, unsigned groups, hipStream_t s)
-{
-    auto go = [&](auto nb) {
-        constexpr int NB = decltype(nb)::value;
-        if (q_fmt == SNACK_F32)
-            hipLaunchKernelGGL((attend_kernel<FMT, NB, SNACK_F32>), dim3(groups), dim3(kAttendThreads), 0, s, a);
-        else
-            hipLaunchKernelGGL((attend_kernel<FMT, NB, SNACK_BF16>), dim3(groups), dim3(kAttendThreads), 0, s, a);
-    };
-    switch (a.c.nb) {
-    case 1: go(std::integral_constant<int, 1>{}); break;
-    case 2: go(std::integral_constant<int, 2>{}); break;
-    case 3: go(std::integral_constant<int, 3>{}); break;
-    case 4: go(std::integral_constant<int, 4>{}); break;
-    case 6: go(std::integral_constant<int, 6>{}); break;
-    default: go(std::integral_constant<int, 8>{}); break;
-    }
-    SNACK_HIP(hipGetLastError());
-    return SNACK_OK;
-}
+enum AttendKind : int { kFew = 0, kMany64, kMany128 };
+constexpr int attend_rows(int kind) { return kind == kFew ? kQueries : kind == kMany64 ? 64 : 128; }
+
 // one file a format: attend_int8.hip, attend_e4m3.hip, attend_e2m1.hip
-extern template snack_status launch_attend<SNACK_INT8>(const AttendArgs&, int, unsigned, hipStream_t);
-extern template snack_status launch_attend<SNACK_E4M3>(const AttendArgs&, int, unsigned, hipStream_t);
-extern template snack_status launch_attend<SNACK_E2M1>(const AttendArgs&, int, unsigned, hipStream_t);
+template <int FMT>
+snack_status launch_attend(const AttendArgs& a, int q_fmt, int kind, unsigned groups, hipStream_t s);
+extern template snack_status launch_attend<SNACK_INT8>(const AttendArgs&, int, int, unsigned, hipStream_t);
+extern template snack_status launch_attend<SNACK_E4M3>(const AttendArgs&, int, int, unsigned, hipStream_t);
+extern template snack_status launch_attend<SNACK_E2M1>(const AttendArgs&, int, int, unsigned, hipStream_t);
 
 }  // namespace snack

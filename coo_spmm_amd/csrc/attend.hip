@@ -10,21 +10,41 @@ constexpr int kGroups = 512;   // workgroups at most: two a compute unit
 
 // what the launches need to know of a call before its lengths, which only the device knows
 struct Plan {
+    int kind;
     unsigned groups;
+    int64_t part;     // floats of the partial results
     int64_t bytes;
 };
 
-Plan make_plan(const CacheView& c, int64_t units, int64_t width)
+// by the queries of a cache head that a sequence has on average
+int attend_kind(int nb, int64_t queries)
 {
-    // the tiles that there can be at most (both factors below 2^31)
+    if (queries <= kQueries) return kFew;
+    return queries <= 64 || nb > 4 ? kMany64 : kMany128;
+}
+
+Plan make_plan(const CacheView& c, int32_t group, int64_t tokens, int32_t sequences, int64_t width)
+{
+    Plan p;
+    p.kind = attend_kind(c.nb, sequences ? tokens * group / sequences : 0);
+    const int rows = attend_rows(p.kind);
+    // blocks of queries of every sequence and head at most, and their tiles (both below 2^31)
+    const int64_t units = c.heads * (tokens * group / rows + sequences);
     const int64_t tiles = units * (width * c.page_tiles + 1);
     int64_t groups = (tiles + kMinRun - 1) / kMinRun;
     if (groups > kGroups) groups = kGroups;
     if (groups < 1) groups = 1;
-    Plan p;
     p.groups = (unsigned)groups;
-    p.bytes = (int64_t)kGroups * (2 * part_floats(c.nb) * 4 + (int64_t)sizeof(int4));
+    p.part = (int64_t)kGroups * 2 * (rows / 16) * part_floats(c.nb);
+    p.bytes = p.part * 4 + kGroups * (int64_t)sizeof(int4);
     return p;
+}
+
+template <int QT>
+auto join_kernel(int kind)
+{
+    return kind == kFew ? attend_join_kernel<QT, attend_rows(kFew)>
+           : kind == kMany64 ? attend_join_kernel<QT, attend_rows(kMany64)> : attend_join_kernel<QT, attend_rows(kMany128)>;
 }
 
 }  // namespace
@@ -40,7 +60,7 @@ extern "C" snack_status snack_cache_attend_work(const snack_cache* cache, int32_
     if (tokens >= (1ll << 31) || tokens * q_heads >= (1ll << 31)) return SNACK_ERR_UNSUPPORTED;
     CacheView c;
     make_cache_view(cache, &c);
-    *bytes = make_plan(c, 1, 1).bytes;
+    *bytes = make_plan(c, q_heads / cache->heads, tokens, sequences, 1).bytes;
     return SNACK_OK;
 }
 
@@ -68,9 +88,7 @@ extern "C" snack_status snack_cache_attend(const snack_cache* cache, const void*
     AttendArgs a{};
     make_cache_view(cache, &a.c);
     const int32_t group = q_heads / cache->heads;
-    // units: blocks of queries of every sequence and head, at most
-    const int64_t units = cache->heads * (tokens * group / kQueries + sequences);
-    const Plan plan = make_plan(a.c, units, width);
+    const Plan plan = make_plan(a.c, group, tokens, sequences, width);
     if (work_bytes < plan.bytes) return SNACK_ERR_WORKSPACE;
     a.q = Q;
     a.q_row = q_row;
@@ -89,14 +107,14 @@ extern "C" snack_status snack_cache_attend(const snack_cache* cache, const void*
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.causal = causal ? 1 : 0;
     a.part = (float*)work;
-    a.meta = (int4*)((char*)work + (int64_t)kGroups * 2 * part_floats(a.c.nb) * 4);
+    a.meta = (int4*)(a.part + plan.part);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     ProfScope prof(KC_ATTEND, s);
-    if (cache->fmt == SNACK_INT8) SNACK_CHECK(launch_attend<SNACK_INT8>(a, q_fmt, plan.groups, s));
-    else if (cache->fmt == SNACK_E4M3) SNACK_CHECK(launch_attend<SNACK_E4M3>(a, q_fmt, plan.groups, s));
-    else SNACK_CHECK(launch_attend<SNACK_E2M1>(a, q_fmt, plan.groups, s));
-    const auto join = q_fmt == SNACK_F32 ? attend_join_kernel<SNACK_F32> : attend_join_kernel<SNACK_BF16>;
-    hipLaunchKernelGGL(join, dim3(plan.groups, 2 * a.c.nb), dim3(kAttendThreads), 0, s, a);
+    if (cache->fmt == SNACK_INT8) SNACK_CHECK(launch_attend<SNACK_INT8>(a, q_fmt, plan.kind, plan.groups, s));
+    else if (cache->fmt == SNACK_E4M3) SNACK_CHECK(launch_attend<SNACK_E4M3>(a, q_fmt, plan.kind, plan.groups, s));
+    else SNACK_CHECK(launch_attend<SNACK_E2M1>(a, q_fmt, plan.kind, plan.groups, s));
+    const auto join = q_fmt == SNACK_F32 ? join_kernel<SNACK_F32>(plan.kind) : join_kernel<SNACK_BF16>(plan.kind);
+    hipLaunchKernelGGL(join, dim3(plan.groups, 2 * a.c.nb, attend_rows(plan.kind) / 16), dim3(kAttendThreads), 0, s, a);
     SNACK_HIP(hipGetLastError());
     return SNACK_OK;
 }
