@@ -32,6 +32,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kAttendWaves = 4;
 constexpr int kAttendThreads = kAttendWaves * kWave;
 constexpr int kQueries = 16;          // queries of a unit
+constexpr int kAttendGroups = 512;   // workgroups at most: two a compute unit
 constexpr int kMinRun = 4;            // tiles of a workgroup at least: one a wavefront
 constexpr float kRaise = 8.0f;        // a running maximum is raised when a score passes it by a factor of 2^8
 
@@ -50,11 +51,26 @@ struct AttendArgs {
     float scale_log2;                 // scale * log2(e)
     int32_t causal;
     float* part;                      // two partial results a workgroup: of the block it goes on with, of the one it starts
-    int4* meta;                       // of the block a workgroup starts and does not end: sequence, block, head, pieces
+    // What the second launch reads, two to a workgroup or (by_unit) to a unit, a block of queries of one cache head, in
+    // the order of the work: of a unit that a workgroup starts and does not end {sequence's first token, block, head,
+    // pieces}, {its queries of a head, the workgroup}, else no pieces.  The last: how many units there are.
+    int4* meta;
+    int32_t by_unit;
+    int32_t meta_last;
 };
 
 // floats of a partial result of 16 queries: the output's, then maximum and sum of every query
 __host__ __device__ constexpr int part_floats(int nb) { return 2 * nb * 256 + 2 * kQueries; }
+
+// What nothing writes while the kernel runs, read by scalar loads where the address is the same for a wavefront (they
+// do not queue behind the vector loads in flight).
+template <typename T>
+using Fixed = const __attribute__((address_space(4))) T*;
+template <typename T>
+__device__ inline Fixed<T> fixed(const T* p)
+{
+    return (Fixed<T>)(uintptr_t)p;
+}
 
 // a sequence of the call
 struct Seq {
@@ -221,17 +237,19 @@ __device__ inline int64_t count_work(const AttendArgs& a, Schedule<THREADS>& l, 
     group_scan<THREADS>(w * a.c.heads, l.work, &total);
     return total;
 }
-// the block that has tile `pos` of them all; before: the tiles before that block
+// the block that has tile `pos` of them all; before: the tiles before that block, index: the blocks before it
 template <int THREADS, int ROWS>
 __device__ inline Cursor find_work(const AttendArgs& a, const Schedule<THREADS>& l, int32_t all_blocks, int64_t pos,
-                                   int64_t* before)
+                                   int64_t* before, int32_t* index)
 {
     const int th = last_at_most<THREADS>(l.work, pos);
     const int32_t run = (all_blocks + THREADS - 1) / THREADS;
     Cursor c = find_block<THREADS, ROWS>(a, l, th * run);
     int64_t at = l.work[th];
+    *index = th * run;
     while (pos >= at + (int64_t)c.tiles * a.c.heads) {
         at += (int64_t)c.tiles * a.c.heads;
+        ++*index;
         next_block<ROWS>(a, c);
     }
     *before = at;
@@ -252,6 +270,16 @@ __device__ inline float query_sum(float x)
     x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
     const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// the largest of eight, a NaN left out: the median of two numbers and infinity is their maximum, and takes its
+// operands as they are (the library's maximum first quiets what could be a signalling NaN: four instructions more)
+__device__ inline float max8(const float* x)
+{
+    const float inf = __builtin_inff();
+    const float a = __builtin_amdgcn_fmed3f(x[0], x[1], inf), b = __builtin_amdgcn_fmed3f(x[2], x[3], inf);
+    const float c = __builtin_amdgcn_fmed3f(x[4], x[5], inf), d = __builtin_amdgcn_fmed3f(x[6], x[7], inf);
+    return __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(a, b, inf), __builtin_amdgcn_fmed3f(c, d, inf), inf);
 }
 
 // x as a sum of bf16 numbers, truncated one after the other (three hold all of fp32's 24 bits; the last of two
@@ -369,41 +397,39 @@ __device__ inline void load_tile(RawTile<FMT, NB>& r, const uint8_t* tile, int l
     if constexpr (NB % 2) load_words<2>(r.ve + 4 * n4, ev + 16 * n4);
 }
 
-// the K operand of block J of a half
-template <int FMT, int NB, int J>
-__device__ inline bf16x8 key_operand(const uint32_t* k, const uint32_t* ke)
+// the K operand of a block: its words, and the exponent in byte BYTE of e
+template <int FMT, int BYTE>
+__device__ inline bf16x8 key_operand(const uint32_t* k, uint32_t e)
 {
-    const float s = scale_of<FMT, J % 4>(ke[J / 4]);
+    const float s = scale_of<FMT, BYTE>(e);
     u32x4 o;
     if constexpr (four_bits(FMT)) {
-        const uint32_t w = k[J];
-        o = u32x4{decode_byte<0>(w, s), decode_byte<1>(w, s), decode_byte<2>(w, s), decode_byte<3>(w, s)};
+        o = u32x4{decode_byte<0>(k[0], s), decode_byte<1>(k[0], s), decode_byte<2>(k[0], s), decode_byte<3>(k[0], s)};
     } else {
-        const uint32_t a = k[2 * J], b = k[2 * J + 1];
-        o = u32x4{decode_half<FMT, 0>(a, s), decode_half<FMT, 1>(a, s), decode_half<FMT, 0>(b, s),
-                  decode_half<FMT, 1>(b, s)};
+        o = u32x4{decode_half<FMT, 0>(k[0], s), decode_half<FMT, 1>(k[0], s), decode_half<FMT, 0>(k[1], s),
+                  decode_half<FMT, 1>(k[1], s)};
     }
     return __builtin_bit_cast(bf16x8, o);
 }
-// the V operands of block B: features 0..15 of it, and 16..31
-template <int FMT, int NB, int B>
+// the V operands of a block: features 0..15 of it, and 16..31
+template <int FMT>
 __device__ inline void value_operands(const uint32_t* v, const uint32_t* ve, bf16x8& lo, bf16x8& hi)
 {
-    const uint32_t e0 = ve[2 * B], e1 = ve[2 * B + 1];
+    const uint32_t e0 = ve[0], e1 = ve[1];
     const float s[8] = {scale_of<FMT, 0>(e0), scale_of<FMT, 1>(e0), scale_of<FMT, 2>(e0), scale_of<FMT, 3>(e0),
                         scale_of<FMT, 0>(e1), scale_of<FMT, 1>(e1), scale_of<FMT, 2>(e1), scale_of<FMT, 3>(e1)};
     u32x4 a, b;
     if constexpr (FMT == SNACK_INT8) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const uint32_t w = v[4 * B + r];
+            const uint32_t w = v[r];
             a[r] = pack_bf16((float)(int8_t)(w & 0xFFu) * s[2 * r], (float)(int8_t)(w >> 16 & 0xFFu) * s[2 * r + 1]);
             b[r] = pack_bf16((float)(int8_t)(w >> 8 & 0xFFu) * s[2 * r], (float)(int8_t)(w >> 24) * s[2 * r + 1]);
         }
     } else {
         uint32_t w[8];   // both features of one token each
         if constexpr (four_bits(FMT)) {
-            const uint32_t x = v[2 * B], y = v[2 * B + 1];
+            const uint32_t x = v[0], y = v[1];
             w[0] = decode_byte<0>(x, s[0]); w[1] = decode_byte<1>(x, s[1]);
             w[2] = decode_byte<2>(x, s[2]); w[3] = decode_byte<3>(x, s[3]);
             w[4] = decode_byte<0>(y, s[4]); w[5] = decode_byte<1>(y, s[5]);
@@ -411,8 +437,8 @@ __device__ inline void value_operands(const uint32_t* v, const uint32_t* ve, bf1
         } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                w[2 * r] = decode_half<FMT, 0>(v[4 * B + r], s[2 * r]);
-                w[2 * r + 1] = decode_half<FMT, 1>(v[4 * B + r], s[2 * r + 1]);
+                w[2 * r] = decode_half<FMT, 0>(v[r], s[2 * r]);
+                w[2 * r + 1] = decode_half<FMT, 1>(v[r], s[2 * r + 1]);
             }
         }
 #pragma unroll
@@ -437,6 +463,13 @@ __device__ inline void unroll(F f)
 
 // the first n of 8 tokens' bytes of a word pair kept, n within 0..8
 __device__ inline uint64_t first_bytes(int n) { return n >= 8 ? ~0ull : n <= 0 ? 0ull : (1ull << (8 * n)) - 1; }
+
+// how many of the lane's eight tokens base + 8 g + 0..7 come up to `limit`
+__device__ inline int tokens_seen(int64_t limit, int64_t base, int g)
+{
+    const int64_t n = limit - base - 8 * g + 1;
+    return n > 8 ? 8 : n < 0 ? 0 : (int)n;
+}
 
 // A V block's codes and exponents of the tokens whose byte is not in m become 0.
 template <int FMT>
@@ -491,6 +524,46 @@ __device__ inline Row get_row(const AttendArgs& a, int32_t h, uint32_t row)
     return Row{(int32_t)i, (int32_t)(h * a.by_group.d + (row - i * a.by_group.d))};
 }
 
+// features f0 + 32 j + 0..7 of a head of d, j < NB, without a branch round each load: where d is a multiple of 8, what
+// is past it is read from the head's start and left out
+template <int NB, typename Q>
+__device__ inline void load_query(f32x8* x, const Q* __restrict__ p, int f0, int d)
+{
+    if (d % 8 == 0) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) x[j] = load8(p + (f0 + 32 * j < d ? f0 + 32 * j : 0), 8);
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (f0 + 32 * j >= d) x[j] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+    } else {
+#pragma unroll
+        for (int j = 0; j < NB; ++j) x[j] = load8(p + f0 + 32 * j, d - f0 - 32 * j);
+    }
+}
+// and their parts as operands
+template <int PARTS, int NB>
+__device__ inline void split_query(bf16x8 (*q)[NB], const f32x8* x)
+{
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[j][i];
+        bf16x8 part[PARTS];
+        split8<PARTS>(y, part);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) q[k][j] = part[k];
+    }
+}
+
+// x / d rounded down, for 0 <= x < 2^52: the quotient in floating point is off by one at most
+__device__ inline int64_t divide(int64_t x, int64_t d)
+{
+    int64_t q = (int64_t)((double)x / (double)d);
+    q -= q * d > x ? 1 : 0;
+    return q + (x - q * d >= d ? 1 : 0);
+}
+
 template <int QT>
 struct QType { using T = float; };
 template <>
@@ -517,61 +590,102 @@ __device__ inline void store_out(void* out, int64_t at, int d, int dims, f32x4 v
     }
 }
 
-// The pieces of the unit that workgroup blockIdx.x of the first launch started, joined; 16 features (blockIdx.y) of 16
-// queries (blockIdx.z).
-template <int QT, int ROWS>
+// The pieces of a unit (blockIdx.x: the unit, or the workgroup that started it), joined: 16 queries (blockIdx.y).  WIDE (few blocks of many pieces each): 16 features (blockIdx.z), the wavefronts sharing the pieces out;
+// else every wavefront some of the features, over all pieces.  Maxima and sums first, so that the pieces' outputs are
+// then added up with known weights and all on their way at once.
+template <int QT, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kAttendThreads) attend_join_kernel(AttendArgs a)
 {
+    __shared__ float red[kAttendThreads / kQueries][kQueries];
     __shared__ f32x4 so[kAttendWaves][kWave];
-    __shared__ float2 sml[kAttendWaves][kQueries];
-    const int4 u = a.meta[blockIdx.x];
-    if (u.w == 0) return;
+    if (a.by_unit && (int)blockIdx.x >= a.meta[a.meta_last].x) return;
+    const int4 u = a.meta[2 * blockIdx.x], u1 = a.meta[2 * blockIdx.x + 1];
+    const uint32_t rows = (uint32_t)u1.x, row0 = (uint32_t)u.y * ROWS + 16 * blockIdx.y;
+    if (u.w == 0 || row0 >= rows) return;
     const int lane = (int)threadIdx.x & (kWave - 1), wave = (int)threadIdx.x / kWave;
-    const int col = lane & 15, g = lane >> 4, i = (int)blockIdx.y;
-    const int size = part_floats(a.c.nb);
-    const Seq s = get_seq(a, u.x);
-    const int32_t h = u.z;
-    const uint32_t rows = (uint32_t)s.nq * a.by_group.d, row = (uint32_t)u.y * ROWS + 16 * blockIdx.z + col;
-    const bool live = row < rows;
-    float m = -__builtin_inff(), sum = 0.0f;
-    f32x4 v = {0, 0, 0, 0};
-    for (int k = wave; k < u.w; k += kAttendWaves) {
-        const float* part = a.part + ((int64_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * (ROWS / 16) + blockIdx.z) * size;
-        float2 ml = make_float2(-__builtin_inff(), 0.0f);
-        f32x4 x = {0, 0, 0, 0};
-        if (live) {
-            ml = *reinterpret_cast<const float2*>(part + 2 * a.c.nb * 256 + 2 * col);
-            x = *reinterpret_cast<const f32x4*>(part + (i * kWave + lane) * 4);
-        }
-        const float n = fmaxf(m, ml.x), ns = n == -__builtin_inff() ? 0.0f : n;
-        const float f0 = __builtin_amdgcn_exp2f(m - ns), f1 = __builtin_amdgcn_exp2f(ml.x - ns);
-        v = v * f0 + x * f1;
-        sum = sum * f0 + ml.y * f1;
-        m = n;
+    const int col = lane & 15, g = lane >> 4;
+    const int size = part_floats(a.c.nb), pieces = u.w, tail = 2 * a.c.nb * 256 + 2 * col;
+    const int i0 = WIDE ? (int)blockIdx.z : wave;     // the first 16 features
+    const bool seen = row0 + col < rows, live = seen && i0 < 2 * a.c.nb;
+    // piece k's results of these queries
+    auto piece = [&](int k) {
+        return a.part + ((int64_t)(2 * (u1.y + k) + (k == 0 ? 1 : 0)) * (ROWS / 16) + blockIdx.y) * size;
+    };
+    auto output = [&](int k, int i) { return *reinterpret_cast<const f32x4*>(piece(k) + (i * kWave + lane) * 4); };
+    // The loads of the first pieces, all at once: each of a chain of loads would take a microsecond.
+    constexpr int kStep = kAttendThreads / kQueries, kMl = 4;     // threads of a query, their pieces
+    constexpr int kX = WIDE ? 16 : 4;
+    const int first = (int)threadIdx.x / kQueries, k0 = WIDE ? wave : 0, ks = WIDE ? kAttendWaves : 1;
+    float2 ml[kMl];
+    f32x4 x[kX];
+    float xm[kX];        // their maxima: a weight is made where it is used (a list of them in LDS keeps workgroups out)
+#pragma unroll
+    for (int r = 0; r < kMl; ++r) {
+        const int k = first + kStep * r;
+        ml[r] = seen && k < pieces ? *reinterpret_cast<const float2*>(piece(k) + tail) : make_float2(-__builtin_inff(), 0.0f);
     }
-    so[wave][lane] = v;
-    if (g == 0) sml[wave][col] = make_float2(m, sum);
+#pragma unroll
+    for (int r = 0; r < kX; ++r) {
+        const int k = k0 + ks * r;
+        x[r] = live && k < pieces ? output(k, i0) : f32x4{0, 0, 0, 0};
+        xm[r] = live && k < pieces ? piece(k)[tail] : -__builtin_inff();
+    }
+    float m = -__builtin_inff();
+#pragma unroll
+    for (int r = 0; r < kMl; ++r) m = fmaxf(m, ml[r].x);
+    if (seen)
+        for (int k = first + kStep * kMl; k < pieces; k += kStep) m = fmaxf(m, piece(k)[tail]);
+    red[first][col] = m;
     __syncthreads();
-    if (wave != 0 || !live) return;
-    m = -__builtin_inff();
 #pragma unroll
-    for (int w = 0; w < kAttendWaves; ++w) m = fmaxf(m, sml[w][col].x);
-    const float ms = m == -__builtin_inff() ? 0.0f : m;
+    for (int i = 0; i < kStep; ++i) m = fmaxf(m, red[i][col]);
+    __syncthreads();
+    const float off = m == -__builtin_inff() ? 0.0f : m;
+    float sum = 0.0f;
+    auto weight = [&](float top) { return __builtin_amdgcn_exp2f(top - off); };
+#pragma unroll
+    for (int r = 0; r < kMl; ++r) sum = fmaf(weight(ml[r].x), ml[r].y, sum);
+    if (seen)
+        for (int k = first + kStep * kMl; k < pieces; k += kStep) {
+            const float2 p = *reinterpret_cast<const float2*>(piece(k) + tail);
+            sum = fmaf(weight(p.x), p.y, sum);
+        }
+    red[first][col] = sum;
+    __syncthreads();
     sum = 0.0f;
-    v = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < kAttendWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(sml[w][col].x - ms);
-        sum = fmaf(f, sml[w][col].y, sum);
-        v += so[w][lane] * f;
+    for (int i = 0; i < kStep; ++i) sum += red[i][col];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const Row mine = get_row(a, u.z, min(row0 + col, rows - 1));
+    const int64_t at = ((int64_t)(u.x + mine.i) * a.hq + mine.head) * a.c.d;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < kX; ++r) v += x[r] * weight(xm[r]);
+    if (live)
+        for (int k = k0 + ks * kX; k < pieces; k += ks) v += output(k, i0) * weight(piece(k)[tail]);
+    if constexpr (WIDE) {
+        so[wave][lane] = v;
+        __syncthreads();
+        if (wave != 0 || !live) return;
+#pragma unroll
+        for (int w = 1; w < kAttendWaves; ++w) v += so[w][lane];
+        store_out<QT>(a.out, at, 16 * i0 + 4 * g, a.c.d, v * inv);
+    } else {
+        if (!live) return;
+        for (int i = i0;;) {
+            store_out<QT>(a.out, at, 16 * i + 4 * g, a.c.d, v * inv);
+            i += kAttendWaves;
+            if (i >= 2 * a.c.nb) break;
+            v = f32x4{0, 0, 0, 0};
+#pragma unroll 4
+            for (int k = 0; k < pieces; ++k) v += output(k, i) * weight(piece(k)[tail]);
+        }
     }
-    const Row mine = get_row(a, h, row);
-    const int64_t at = ((int64_t)(s.first + mine.i) * a.hq + mine.head) * a.c.d;
-    store_out<QT>(a.out, at, 16 * i + 4 * g, a.c.d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
 }
 
-enum AttendKind : int { kFew = 0, kMany64, kMany128 };
-constexpr int attend_rows(int kind) { return kind == kFew ? kQueries : kind == kMany64 ? 64 : 128; }
+// which kernel: by the queries of a block
+enum AttendKind : int { kFew = 0, kMany64, kMany256 };
+constexpr int attend_rows(int kind) { return kQueries << (2 * kind); }
 
 // one file a format: attend_int8.hip, attend_e4m3.hip, attend_e2m1.hip
 template <int FMT>

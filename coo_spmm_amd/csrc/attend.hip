@@ -6,21 +6,24 @@
 namespace snack {
 namespace {
 
-constexpr int kGroups = 512;   // workgroups at most: two a compute unit
-
 // what the launches need to know of a call before its lengths, which only the device knows
 struct Plan {
     int kind;
     unsigned groups;
+    int64_t units;    // at most
+    int most;         // workgroups at most, and entries of the pieces' list
     int64_t part;     // floats of the partial results
     int64_t bytes;
 };
 
-// by the queries of a cache head that a sequence has on average
+// By the queries of a cache head that a sequence has on average.  Measured (us, both launches, int8, 32 query and 8
+// cache heads of 128, 8192 tokens; blocks of 16 : 64 : 256 queries): 4 sequences of 24 queries a head 37 : 32 : -, one
+// of 96 32 : 29 : 32, of 192 49 : 39 : 35, of 2048 (bf16) - : 192 : 125, (fp32) - : 278 : 249.  Blocks of 256 of heads
+// past 128 features would not fit the registers.
 int attend_kind(int nb, int64_t queries)
 {
     if (queries <= kQueries) return kFew;
-    return queries <= 64 || nb > 4 ? kMany64 : kMany128;
+    return queries <= 128 || nb > 4 ? kMany64 : kMany256;
 }
 
 Plan make_plan(const CacheView& c, int32_t group, int64_t tokens, int32_t sequences, int64_t width)
@@ -28,23 +31,38 @@ Plan make_plan(const CacheView& c, int32_t group, int64_t tokens, int32_t sequen
     Plan p;
     p.kind = attend_kind(c.nb, sequences ? tokens * group / sequences : 0);
     const int rows = attend_rows(p.kind);
+    // one workgroup of the largest kind a compute unit, two of the others
+    const int most = p.kind == kMany256 ? kAttendGroups / 2 : kAttendGroups;
     // blocks of queries of every sequence and head at most, and their tiles (both below 2^31)
-    const int64_t units = c.heads * (tokens * group / rows + sequences);
-    const int64_t tiles = units * (width * c.page_tiles + 1);
+    p.units = c.heads * (tokens * group / rows + sequences);
+    const int64_t tiles = p.units * (width * c.page_tiles + 1);
     int64_t groups = (tiles + kMinRun - 1) / kMinRun;
-    if (groups > kGroups) groups = kGroups;
+    if (groups > most) groups = most;
     if (groups < 1) groups = 1;
     p.groups = (unsigned)groups;
-    p.part = (int64_t)kGroups * 2 * (rows / 16) * part_floats(c.nb);
-    p.bytes = p.part * 4 + kGroups * (int64_t)sizeof(int4);
+    p.part = (int64_t)most * 2 * (rows / 16) * part_floats(c.nb);
+    p.most = most;
+    p.bytes = p.part * 4 + (2 * most + 1) * (int64_t)sizeof(int4);
     return p;
 }
 
-template <int QT>
-auto join_kernel(int kind)
+template <int QT, int ROWS>
+void join(const AttendArgs& a, const Plan& p, hipStream_t s)
 {
-    return kind == kFew ? attend_join_kernel<QT, attend_rows(kFew)>
-           : kind == kMany64 ? attend_join_kernel<QT, attend_rows(kMany64)> : attend_join_kernel<QT, attend_rows(kMany128)>;
+    const unsigned entries = a.by_unit ? (unsigned)p.units : p.groups;
+    if (p.units * 8 <= p.groups)     // many pieces of each
+        hipLaunchKernelGGL((attend_join_kernel<QT, ROWS, true>), dim3(entries, ROWS / 16, 2 * a.c.nb), dim3(kAttendThreads), 0, s, a);
+    else
+        hipLaunchKernelGGL((attend_join_kernel<QT, ROWS, false>), dim3(entries, ROWS / 16), dim3(kAttendThreads), 0, s, a);
+}
+template <int QT>
+void join(const AttendArgs& a, const Plan& p, hipStream_t s)
+{
+    switch (p.kind) {
+    case kFew: join<QT, attend_rows(kFew)>(a, p, s); break;
+    case kMany64: join<QT, attend_rows(kMany64)>(a, p, s); break;
+    default: join<QT, attend_rows(kMany256)>(a, p, s); break;
+    }
 }
 
 }  // namespace
@@ -108,13 +126,15 @@ extern "C" snack_status snack_cache_attend(const snack_cache* cache, const void*
     a.causal = causal ? 1 : 0;
     a.part = (float*)work;
     a.meta = (int4*)(a.part + plan.part);
+    a.by_unit = plan.units <= plan.most;
+    a.meta_last = 2 * plan.most;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     ProfScope prof(KC_ATTEND, s);
     if (cache->fmt == SNACK_INT8) SNACK_CHECK(launch_attend<SNACK_INT8>(a, q_fmt, plan.kind, plan.groups, s));
     else if (cache->fmt == SNACK_E4M3) SNACK_CHECK(launch_attend<SNACK_E4M3>(a, q_fmt, plan.kind, plan.groups, s));
     else SNACK_CHECK(launch_attend<SNACK_E2M1>(a, q_fmt, plan.kind, plan.groups, s));
-    const auto join = q_fmt == SNACK_F32 ? join_kernel<SNACK_F32>(plan.kind) : join_kernel<SNACK_BF16>(plan.kind);
-    hipLaunchKernelGGL(join, dim3(plan.groups, 2 * a.c.nb, attend_rows(plan.kind) / 16), dim3(kAttendThreads), 0, s, a);
+    if (q_fmt == SNACK_F32) join<SNACK_F32>(a, plan, s);
+    else join<SNACK_BF16>(a, plan, s);
     SNACK_HIP(hipGetLastError());
     return SNACK_OK;
 }
