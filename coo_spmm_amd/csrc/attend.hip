@@ -33,10 +33,11 @@ Plan make_plan(const CacheView& c, int32_t group, int64_t tokens, int32_t sequen
     const int rows = attend_rows(p.kind);
     // one workgroup of the largest kind a compute unit, two of the others
     const int most = p.kind == kMany256 ? kAttendGroups / 2 : kAttendGroups;
-    // blocks of queries of every sequence and head at most, and their tiles (both below 2^31)
+    // blocks of queries of every sequence and head at most, and their work (both factors below 2^31)
     p.units = c.heads * (tokens * group / rows + sequences);
-    const int64_t tiles = p.units * (width * c.page_tiles + 1);
-    int64_t groups = (tiles + kMinRun - 1) / kMinRun;
+    const int cost = p.kind == kFew ? kFewCost : kManyCost;
+    const int64_t work = p.units * (width * c.page_tiles + 1 + cost);
+    int64_t groups = (work + kMinRun - 1) / kMinRun;
     if (groups > most) groups = most;
     if (groups < 1) groups = 1;
     p.groups = (unsigned)groups;

@@ -9,6 +9,8 @@ template <int FMT, int NB, int QT>
 __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel(AttendArgs a)
 {
     constexpr int QP = QT == SNACK_F32 ? 3 : 1, PP = QT == SNACK_F32 ? 3 : 2;
+    constexpr int DEPTH = 2;     // tiles of a wavefront in registers: the one in use, one on its way (three: 51 against 48 us
+                                 // for 64 streams of up to 4096 tokens, whose last tile is then loaded once more)
     using Q = typename QType<QT>::T;
     __shared__ Schedule<kAttendThreads> sched;
     __shared__ f32x4 so[kAttendWaves][2 * NB][kWave];
@@ -30,12 +32,14 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
     int64_t before;
     int32_t index;
     Cursor c = find_work<kAttendThreads, kQueries>(a, sched, all_blocks, pos, &before, &index);
-    int32_t h = (int32_t)divide(pos - before, c.tiles);
-    int32_t t0 = (int32_t)(pos - before - (int64_t)h * c.tiles);
+    int32_t h = (int32_t)divide(pos - before, c.cost);
+    int32_t o0 = (int32_t)(pos - before - (int64_t)h * c.cost);     // within the unit
 
     while (pos < end) {
         const Seq s = c.s;
-        const int32_t b = c.b, t1 = (int32_t)min((int64_t)c.tiles, t0 + (end - pos));
+        const int32_t b = c.b, o1 = (int32_t)min((int64_t)c.cost, o0 + (end - pos));
+        const int32_t t0 = max(o0 - unit_cost<kQueries>(), 0), t1 = max(o1 - unit_cost<kQueries>(), 0);
+        if (t1 == 0) break;      // the next workgroup starts it
         const uint32_t rows = (uint32_t)s.nq * a.by_group.d, row0 = (uint32_t)c.k * kQueries;
         const uint32_t row = row0 + col;
         const bool live = row < rows;
@@ -44,13 +48,6 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
         const int64_t past = a.causal ? (int64_t)s.len - s.nq : (int64_t)s.len - 1;
         const int64_t limit = a.causal ? past + mine.i : past;
         const int64_t least = a.causal ? past + fast_quot(a.by_group, row0) : past;
-
-        bf16x8 q[QP][NB];
-        {
-            f32x8 x[NB];
-            load_query<NB>(x, (const Q*)a.q + (int64_t)(s.first + mine.i) * a.q_row + (int64_t)mine.head * a.q_head, 8 * g, a.c.d);
-            split_query<QP, NB>(q, x);
-        }
 
         f32x4 o[2 * NB];
 #pragma unroll
@@ -68,20 +65,34 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
             return a.c.data + (int64_t)(ok ? page : 0) * a.c.page_bytes +
                    ((int64_t)h * a.c.page_tiles + (t - p * a.c.page_tiles)) * a.c.record;
         };
-        RawTile<FMT, NB> cur, next;
-        int32_t t = t0 + wave;
-        int32_t page = 0, page1 = 0;
-        if (t < t1) {
-            page = page_of(t);
-            page1 = page_of(min(t + kAttendWaves, t1 - 1));
-            load_tile(cur, tile_at(t, page), lane);
+        // tiles t0 + wave, + 4, ... up to t1; the last again where there is none
+        auto at_most = [&](int32_t t) { return min(t, t1 - 1); };
+        auto is_bad = [&](int32_t p) { return p < 0 || p >= a.pages; };
+        RawTile<FMT, NB> raw[DEPTH];
+        uint32_t bad_tiles = 0;      // bit i: the i-th tile from the present one on has no page
+        int32_t page;
+        {
+            int32_t p[DEPTH];
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) p[i] = page_of(at_most(t0 + wave + kAttendWaves * i));
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) {
+                load_tile(raw[i], tile_at(at_most(t0 + wave + kAttendWaves * i), p[i]), lane);
+                bad_tiles |= is_bad(p[i]) ? 1u << i : 0u;
+                // in this order: what is waited for in the loop is counted in loads behind it, by both ways into it
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            page = page_of(at_most(t0 + wave + kAttendWaves * DEPTH));
         }
-        for (; t < t1; t += kAttendWaves) {
-            const int32_t tn = min(t + kAttendWaves, t1 - 1);
-            load_tile(next, tile_at(tn, page1), lane);
-            const int32_t page2 = page_of(min(t + 2 * kAttendWaves, t1 - 1));
+        bf16x8 q[QP][NB];
+        {
+            f32x8 x[NB];
+            load_query<NB>(x, (const Q*)a.q + (int64_t)(s.first + mine.i) * a.q_row + (int64_t)mine.head * a.q_head, 8 * g, a.c.d);
+            split_query<QP, NB>(q, x);
+        }
+        auto multiply = [&](int32_t t, RawTile<FMT, NB>& cur) {
             const int64_t base = (int64_t)t * kTile;
-            const bool bad = page < 0 || page >= a.pages;
+            const bool bad = bad_tiles & 1u;
             f32x4 sc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
             unroll<NB>([&](auto jc) {
                 constexpr int j = decltype(jc)::value;
@@ -147,10 +158,17 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
                     o[2 * blk + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, p[i], o[2 * blk + 1], 0, 0, 0);
                 }
             });
-            cur = next;
-            page = page1;
-            page1 = page2;
-        }
+        };
+        // The same registers for a tile each time round (a copy would wait for it), and one way out of the loop.
+        for (int32_t t = t0 + wave; t < t1; t += kAttendWaves * DEPTH)
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) {
+                const int32_t at = t + kAttendWaves * i;
+                if (at < t1) multiply(at, raw[i]);
+                load_tile(raw[i], tile_at(at_most(at + kAttendWaves * DEPTH), page), lane);
+                bad_tiles = bad_tiles >> 1 | (is_bad(page) ? 1u << (DEPTH - 1) : 0u);
+                page = page_of(at_most(at + kAttendWaves * (DEPTH + 1)));
+            }
         // the wavefronts' results of the unit, joined
         l = query_sum(l);
         if (g == 0) sml[wave][col] = make_float2(mc, l);
@@ -184,14 +202,14 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
             *reinterpret_cast<float2*>(part + 2 * NB * 256 + 2 * col) = make_float2(m, sum);
         if (t0 == 0 && threadIdx.x == 0 && (a.by_unit || !whole)) {
             // pieces: this one and those of the workgroups up to the one that has the unit's last tile
-            const int64_t rest = c.tiles - t1;
+            const int64_t rest = c.cost - o1;
             int4* m = a.meta + 2 * (a.by_unit ? index * a.c.heads + h : (int32_t)blockIdx.x);
             m[0] = make_int4(s.first, c.k, h, whole ? 0 : (int32_t)(1 + divide(rest + run - 1, run)));
             m[1] = make_int4((int32_t)rows, (int32_t)blockIdx.x, 0, 0);
         }
         __syncthreads();
-        pos += t1 - t0;
-        t0 = 0;
+        pos += o1 - o0;
+        o0 = 0;
         if (++h == a.c.heads) {
             h = 0;
             ++index;
@@ -293,12 +311,14 @@ __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_k
     int64_t before;
     int32_t index;
     Cursor c = find_work<THREADS, ROWS>(a, sched, all_blocks, pos, &before, &index);
-    int32_t h = (int32_t)divide(pos - before, c.tiles);
-    int32_t t0 = (int32_t)(pos - before - (int64_t)h * c.tiles);
+    int32_t h = (int32_t)divide(pos - before, c.cost);
+    int32_t o0 = (int32_t)(pos - before - (int64_t)h * c.cost);     // within the unit
 
     while (pos < end) {
         const Seq s = c.s;
-        const int32_t b = c.b, t1 = (int32_t)min((int64_t)c.tiles, t0 + (end - pos));
+        const int32_t b = c.b, o1 = (int32_t)min((int64_t)c.cost, o0 + (end - pos));
+        const int32_t t0 = max(o0 - unit_cost<ROWS>(), 0), t1 = max(o1 - unit_cost<ROWS>(), 0);
+        if (t1 == 0) break;      // the next workgroup starts it
         const uint32_t rows = (uint32_t)s.nq * a.by_group.d, row0 = (uint32_t)c.k * ROWS;
         const int64_t past = a.causal ? (int64_t)s.len - s.nq : (int64_t)s.len - 1;
         // wavefront w has the groups of 16 queries w, w + W: a block of few queries is still shared out
@@ -561,13 +581,13 @@ __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_k
             }
         }
         if (t0 == 0 && threadIdx.x == 0 && (a.by_unit || !whole)) {
-            const int64_t rest = c.tiles - t1;
+            const int64_t rest = c.cost - o1;
             int4* m = a.meta + 2 * (a.by_unit ? index * a.c.heads + h : (int32_t)blockIdx.x);
             m[0] = make_int4(s.first, c.k, h, whole ? 0 : (int32_t)(1 + divide(rest + run - 1, run)));
             m[1] = make_int4((int32_t)rows, (int32_t)blockIdx.x, 0, 0);
         }
-        pos += t1 - t0;
-        t0 = 0;
+        pos += o1 - o0;
+        o0 = 0;
         if (++h == a.c.heads) {
             h = 0;
             ++index;
