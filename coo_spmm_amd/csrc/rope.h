@@ -51,6 +51,7 @@ __device__ inline T lanes_sum(T x)
     if constexpr (LPR >= 8) x += dpp<0x141>(x);
     if constexpr (LPR >= 16) x += dpp<0x140>(x);
     if constexpr (LPR >= 32) x += __shfl_xor(x, 16, kWave);
+    if constexpr (LPR >= 64) x += __shfl_xor(x, 32, kWave);
     return x;
 }
 
@@ -182,6 +183,99 @@ template <typename V>
 __device__ inline V swap_pairs(V v)
 {
     return __builtin_shufflevector(v, v, 1, 0, 3, 2, 5, 4, 7, 6);
+}
+
+// The same head with a lane holding whole pairs: four pairs (half layout: features 4 l..4 l + 3 and their partners r
+// further; pairs layout: eight in a row) on the first ceil(r / 4) lanes, eight of the other features on the lanes behind
+// them.  Nothing is read for a partner's sake, and a lane takes four angles for its eight features.
+struct Eight {
+    f32x4 a, b;
+};
+struct Spot8 {
+    int a, b;     // first features of the two fours
+    int na, nb;   // how many of each exist
+    bool turned;
+};
+__device__ inline Spot8 find_spot8(int lane, int d, int r, int layout)
+{
+    const int turning = (r + 3) >> 2;
+    Spot8 s;
+    s.turned = lane < turning;
+    if (s.turned && layout == SNACK_ROPE_HALF) {
+        s.a = 4 * lane;
+        s.b = r + s.a;
+        s.na = s.nb = min(4, r - s.a);
+    } else {
+        const int end = s.turned ? 2 * r : d;
+        s.a = s.turned ? 8 * lane : 2 * r + 8 * (lane - turning);
+        s.b = s.a + 4;
+        s.na = max(0, min(4, end - s.a));
+        s.nb = max(0, min(4, end - s.b));
+    }
+    return s;
+}
+inline int pair_lanes(int d, int r)
+{
+    const int n = (r + 3) / 4 + (d - 2 * r + 7) / 8;
+    return n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
+}
+// Four of n numbers from i on, without a branch round the load where n >= 4: the last four where fewer are left, moved
+// into place.  Those past the m-th are 0.
+__device__ inline f32x4 raw4(const float* p) { return *reinterpret_cast<const f32x4u*>(p); }
+__device__ inline f32x4 raw4(const uint16_t* p)
+{
+    const u16x4u h = *reinterpret_cast<const u16x4u*>(p);
+    return f32x4{bf16_value(h.x), bf16_value(h.y), bf16_value(h.z), bf16_value(h.w)};
+}
+template <typename X>
+__device__ inline f32x4 take4(const X* __restrict__ p, int i, int n, int m)
+{
+    f32x4 v = {0, 0, 0, 0};
+    if (n < 4) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (k < m) v[k] = load1(p + i + k);
+        return v;
+    }
+    const int over = i - (n - 4);
+    v = raw4(p + (over > 0 ? n - 4 : i));
+    if (over > 0) v = f32x4{over == 1 ? v.y : over == 2 ? v.z : v.w, over == 1 ? v.z : v.w, v.w, 0.0f};
+    return f32x4{m > 0 ? v.x : 0.0f, m > 1 ? v.y : 0.0f, m > 2 ? v.z : 0.0f, m > 3 ? v.w : 0.0f};
+}
+template <typename X>
+__device__ inline Eight take8(const X* __restrict__ p, const Spot8& s, int d)
+{
+    return Eight{take4(p, s.a, d, s.na), take4(p, s.b, d, s.nb)};
+}
+__device__ inline void put4(float* __restrict__ p, f32x4 v, int m)
+{
+    if (m >= 4) *reinterpret_cast<f32x4u*>(p) = v;
+    else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < m) p[i] = v[i];
+}
+__device__ inline void put4(uint16_t* __restrict__ p, f32x4 v, int m)
+{
+    if (m >= 4) *reinterpret_cast<u16x4u*>(p) = u16x4u{bf16_bits(v.x), bf16_bits(v.y), bf16_bits(v.z), bf16_bits(v.w)};
+    else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < m) p[i] = bf16_bits(v[i]);
+}
+// cos and sin of the lane's four pairs (1 and 0 where it has none); NaN for a position outside the table
+struct Angles {
+    f32x4 c, s;
+};
+__device__ inline Angles take_angles(const Rotation& ro, int pos, int lane, bool turned)
+{
+    const bool ok = (uint32_t)pos < ro.positions;
+    const float* row = ro.table + (int64_t)(ok ? pos : 0) * (2 * ro.r);
+    const int i = turned ? 4 * lane : 0, m = turned ? min(4, ro.r - i) : 0;
+    Angles t{take4(row, i, ro.r, m), take4(row + ro.r, i, ro.r, m)};
+    const float one = ok ? 1.0f : __builtin_nanf("");
+    if (!turned || !ok) t.c = f32x4{one, one, one, one};
+    return t;
 }
 
 // 1 / sqrt(a): the instruction's 2^-14 or better brought to 64 bits by three Newton steps

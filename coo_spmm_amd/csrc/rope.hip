@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxGroups = 2048;    // workgroups (and partial rows) of a gradient at most
-constexpr int kSumThreads = 1024;
+constexpr int kSumThreads = 1024, kSumCols = 8;
 
 __global__ void __launch_bounds__(kThreads) table_kernel(float* __restrict__ T, uint32_t total, FastDiv by_r,
                                                          double log2_base, double factor, double trained, double low,
@@ -55,109 +55,133 @@ qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rota
 {
     __shared__ float sums[kThreads * 8];
     const bool second = blockIdx.x >= q.groups;
-    const BwdPart& a = second ? k : q;
+    const BwdPart a = second ? k : q;
     const uint32_t group = second ? blockIdx.x - q.groups : blockIdx.x;
     constexpr int kRows = kThreads / LPR;
-    const int lane = (int)threadIdx.x % LPR, f0 = 8 * lane;
+    const int lane = (int)threadIdx.x % LPR;
+    const Spot8 at8 = find_spot8(lane, d, ro.r, ro.layout);
     const uint32_t first = group * a.run, last = min(a.x.rows, first + a.run);
-    f32x8 dg = {0, 0, 0, 0, 0, 0, 0, 0};
+    Eight gain{{0, 0, 0, 0}, {0, 0, 0, 0}}, dg = gain;
+    if (a.gain) gain = take8(a.gain, at8, d);
     // whole wavefronts stay in the loop: the sums over lanes take every lane
     for (uint32_t at = first; at < last; at += kRows) {
         const uint32_t row = at + threadIdx.x / LPR;
         const bool live = row < last;
         const uint32_t rr = live ? row : last - 1;
         const uint32_t token = fast_quot(a.x.heads, rr), h = rr - token * a.x.heads.d;
-        const Y* gp = (const Y*)a.g.p + (int64_t)token * a.g.row + (int64_t)h * a.g.head;
-        f32x8 dy = load8(gp + f0, d - f0);
-        f32x8 x = {0, 0, 0, 0, 0, 0, 0, 0}, gain = x;
-        if (a.gain) {
-            x = load8((const X*)a.x.p + (int64_t)token * a.x.row + (int64_t)h * a.x.head + f0, d - f0);
-            gain = load8(a.gain + f0, d - f0);
-        }
+        const int p = ro.table ? pos[token] : 0;
+        Eight dy = take8((const Y*)a.g.p + (int64_t)token * a.g.row + (int64_t)h * a.g.head, at8, d);
+        Eight x{{0, 0, 0, 0}, {0, 0, 0, 0}};
+        if (a.gain) x = take8((const X*)a.x.p + (int64_t)token * a.x.row + (int64_t)h * a.x.head, at8, d);
         if (ro.table) {
-            const int p = pos[token];
-            if (f0 < 2 * ro.r) {
-                const Turn t = load_turn(ro, p, f0, true);
-                const f32x8 o = ro.layout == SNACK_ROPE_PAIRS ? swap_pairs(dy) : load_partners(ro, gp, f0);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dy[i] = f0 + i < 2 * ro.r ? fmaf(o[i], t.s[i], dy[i] * t.c[i]) : dy[i] * t.c[i];
-            } else if ((uint32_t)p >= ro.positions) {
-                dy *= __builtin_nanf("");
+            const Angles t = take_angles(ro, p, lane, at8.turned);
+            const Eight g = dy;
+            if (ro.layout == SNACK_ROPE_HALF || !at8.turned) {
+                dy.a = g.a * t.c + g.b * t.s;
+                dy.b = g.b * t.c - g.a * t.s;
+            } else {
+                dy.a = f32x4{g.a.x * t.c.x + g.a.y * t.s.x, g.a.y * t.c.x - g.a.x * t.s.x,
+                             g.a.z * t.c.y + g.a.w * t.s.y, g.a.w * t.c.y - g.a.z * t.s.y};
+                dy.b = f32x4{g.b.x * t.c.z + g.b.y * t.s.z, g.b.y * t.c.z - g.b.x * t.s.z,
+                             g.b.z * t.c.w + g.b.w * t.s.w, g.b.w * t.c.w - g.b.z * t.s.w};
+            }
+            if (!at8.turned) {      // what is not turned keeps its own value, whatever its neighbours hold
+                dy.a = g.a * t.c;
+                dy.b = g.b * t.c;
             }
         }
-        f32x8 dx = dy;
+        Eight dx = dy;
         if (a.gain) {
-            const f32x8 w = dy * gain;
+            const f32x4 wa = dy.a * gain.a, wb = dy.b * gain.b;
             // 64 bits: squares of any fp32 value
             double ss = 0.0, ws = 0.0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                ss = fma((double)x[i], (double)x[i], ss);
-                ws = fma((double)w[i], (double)x[i], ws);
+            for (int i = 0; i < 4; ++i) {
+                ss = fma((double)x.a[i], (double)x.a[i], ss);
+                ss = fma((double)x.b[i], (double)x.b[i], ss);
+                ws = fma((double)wa[i], (double)x.a[i], ws);
+                ws = fma((double)wb[i], (double)x.b[i], ws);
             }
             const double r = rsqrt64(fma(lanes_sum<LPR>(ss), inv_d, eps));
             const float rstd = (float)r;
             const float m = (float)(lanes_sum<LPR>(ws) * inv_d * r * r);
-            const f32x8 xh = x * rstd;
-            if (live) dg += dy * xh;
+            if (live) {
+                dg.a += dy.a * (x.a * rstd);
+                dg.b += dy.b * (x.b * rstd);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dx[i] = rstd * fmaf(-x[i], m, w[i]);
+            for (int i = 0; i < 4; ++i) {
+                dx.a[i] = rstd * fmaf(-x.a[i], m, wa[i]);
+                dx.b[i] = rstd * fmaf(-x.b[i], m, wb[i]);
+            }
         }
-        if (live) store8((X*)a.dx + (int64_t)row * d + f0, dx, d - f0);
+        if (live) {
+            X* to = (X*)a.dx + (int64_t)row * d;
+            put4(to + at8.a, dx.a, at8.na);
+            put4(to + at8.b, dx.b, at8.nb);
+        }
     }
     if (!a.part) return;
-    // the lanes of a feature: kRows of them, in order
+    // the threads of a feature: kRows of them, in order
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sums[i * kThreads + (int)threadIdx.x] = dg[i];
+    for (int i = 0; i < 4; ++i) {
+        sums[i * kThreads + (int)threadIdx.x] = dg.a[i];
+        sums[(4 + i) * kThreads + (int)threadIdx.x] = dg.b[i];
+    }
     __syncthreads();
-    for (int f = (int)threadIdx.x; f < d; f += kThreads) {
+    for (int e = (int)threadIdx.x; e < 8 * LPR; e += kThreads) {
+        const Spot8 to = find_spot8(e % LPR, d, ro.r, ro.layout);
+        const int i = e / LPR;
+        if ((i & 3) >= (i < 4 ? to.na : to.nb)) continue;
         float s = 0.0f;
-        for (int j = 0; j < kRows; ++j) s += sums[(f & 7) * kThreads + j * LPR + (f >> 3)];
-        a.part[(int64_t)group * d + f] = s;
+        for (int j = 0; j < kRows; ++j) s += sums[i * kThreads + j * LPR + e % LPR];
+        a.part[(int64_t)group * d + (i < 4 ? to.a : to.b) + (i & 3)] = s;
     }
 }
 
-// dgain[f] = sum over the partial rows, in 64 bits; a workgroup 32 features, its threads 32 runs of rows each
+// dgain[f] = sum over the partial rows, in 64 bits; a workgroup 8 features, its threads 128 runs of rows each
 __global__ void __launch_bounds__(kSumThreads)
 gain_sum_kernel(const float* __restrict__ pq, uint32_t nq, float* __restrict__ gq, const float* __restrict__ pk,
                 uint32_t nk, float* __restrict__ gk, int d)
 {
-    __shared__ double sums[32][33];
+    __shared__ double sums[kSumThreads / kSumCols][kSumCols + 1];
     const bool second = blockIdx.y != 0;
     const float* p = second ? pk : pq;
     const uint32_t n = second ? nk : nq;
     float* out = second ? gk : gq;
     if (!out) return;
-    const int c = (int)threadIdx.x & 31, r = (int)threadIdx.x >> 5, f = (int)blockIdx.x * 32 + c;
+    constexpr uint32_t kRuns = kSumThreads / kSumCols;
+    const int c = (int)threadIdx.x % kSumCols, f = (int)blockIdx.x * kSumCols + c;
+    const uint32_t r = threadIdx.x / kSumCols;
     double s = 0.0;
     if (f < d)
-        for (uint32_t i = r; i < n; i += 32) s += p[(int64_t)i * d + f];
+#pragma unroll 8
+        for (uint32_t i = r; i < n; i += kRuns) s += p[(int64_t)i * d + f];
     sums[r][c] = s;
     __syncthreads();
-    if (r == 0 && f < d) {
-        double t = 0.0;
-        for (int i = 0; i < 32; ++i) t += sums[i][c];
-        out[f] = (float)t;
+    for (uint32_t half = kRuns / 2; half; half >>= 1) {
+        if (r < half) sums[r][c] += sums[r + half][c];
+        __syncthreads();
     }
+    if (r == 0 && f < d) out[f] = (float)sums[0][c];
 }
 
 // workgroups of `rows` heads and the heads of each
-void bwd_split(uint32_t rows, int d, uint32_t most, uint32_t* groups, uint32_t* run)
+void bwd_split(uint32_t rows, int lanes, uint32_t most, uint32_t* groups, uint32_t* run)
 {
-    const uint32_t per = kThreads / head_lanes(d);
+    const uint32_t per = kThreads / lanes;
     const uint32_t units = (rows + per - 1) / per;     // rows a workgroup takes at once
     const uint32_t turns = units ? (units + most - 1) / most : 0;
     *run = turns * per;
     *groups = turns ? (units + turns - 1) / turns : 0;
 }
 // of queries and keys: the workgroups shared out by their heads
-void bwd_splits(uint32_t rq, uint32_t rk, int d, uint32_t* gq, uint32_t* runq, uint32_t* gk, uint32_t* runk)
+void bwd_splits(uint32_t rq, uint32_t rk, int lanes, uint32_t* gq, uint32_t* runq, uint32_t* gk, uint32_t* runk)
 {
     const uint64_t all = (uint64_t)rq + rk;
     const uint32_t mq = all ? (uint32_t)((uint64_t)kMaxGroups * rq / all) : 0;
-    bwd_split(rq, d, mq < 1 ? 1 : mq, gq, runq);
-    bwd_split(rk, d, kMaxGroups - mq < 1 ? 1 : kMaxGroups - mq, gk, runk);
+    bwd_split(rq, lanes, mq < 1 ? 1 : mq, gq, runq);
+    bwd_split(rk, lanes, kMaxGroups - mq < 1 ? 1 : kMaxGroups - mq, gk, runk);
 }
 
 }  // namespace
@@ -243,9 +267,12 @@ extern "C" snack_status snack_qk_rope_bwd_work(int64_t tokens, int32_t q_heads, 
     if (!bytes) return SNACK_ERR_INVALID_ARG;
     SNACK_CHECK(make_heads(nullptr, 0, 0, q_heads, tokens, head_dim, SNACK_F32, &q));
     SNACK_CHECK(make_heads(nullptr, 0, 0, k_heads, tokens, head_dim, SNACK_F32, &k));
-    uint32_t gq, gk, rq, rk;
-    bwd_splits(q.rows, k.rows, head_dim, &gq, &rq, &gk, &rk);
-    *bytes = ((int64_t)gq + gk) * head_dim * 4;
+    // the lanes of a head, and with them the workgroups, depend on the rotation: no more than the workgroups' limit
+    // (each side's share rounded up) or a workgroup for the fewest heads that one takes
+    uint64_t groups = kMaxGroups + 2;
+    const uint64_t fewest = ((uint64_t)q.rows + k.rows + 3) / 4 + 2;
+    if (fewest < groups) groups = fewest;
+    *bytes = (int64_t)groups * head_dim * 4;
     return SNACK_OK;
 }
 
@@ -270,7 +297,8 @@ extern "C" snack_status snack_qk_rope_bwd(const void* Q, int64_t q_row, int64_t 
         (k.x.rows && (!dYk || !dXk || misaligned(dXk, xa) || (k_gain && !K))) || misaligned(q_gain, 4) ||
         misaligned(k_gain, 4) || misaligned(dq_gain, 4) || misaligned(dk_gain, 4) || q_heads + (int64_t)k_heads == 0)
         return SNACK_ERR_INVALID_ARG;
-    bwd_splits(q.x.rows, k.x.rows, head_dim, &q.groups, &q.run, &k.groups, &k.run);
+    const int lanes = pair_lanes(head_dim, ro.r);
+    bwd_splits(q.x.rows, k.x.rows, lanes, &q.groups, &q.run, &k.groups, &k.run);
     if (dq_gain || dk_gain) {
         const int64_t need = ((int64_t)q.groups + k.groups) * head_dim * 4;
         if (need && (!work || misaligned(work, 4))) return SNACK_ERR_INVALID_ARG;
@@ -299,16 +327,17 @@ extern "C" snack_status snack_qk_rope_bwd(const void* Q, int64_t q_row, int64_t 
                 else launch(lanes, uint16_t{}, uint16_t{});
             }
         };
-        switch (head_lanes(head_dim)) {
+        switch (lanes) {
         case 4: types(std::integral_constant<int, 4>{}); break;
         case 8: types(std::integral_constant<int, 8>{}); break;
         case 16: types(std::integral_constant<int, 16>{}); break;
-        default: types(std::integral_constant<int, 32>{}); break;
+        case 32: types(std::integral_constant<int, 32>{}); break;
+        default: types(std::integral_constant<int, 64>{}); break;
         }
         SNACK_HIP(hipGetLastError());
     }
     if (dq_gain || dk_gain) {
-        hipLaunchKernelGGL(gain_sum_kernel, dim3((unsigned)(head_dim + 31) / 32, 2), dim3(kSumThreads), 0, s, q.part,
+        hipLaunchKernelGGL(gain_sum_kernel, dim3((unsigned)((head_dim + kSumCols - 1) / kSumCols), 2), dim3(kSumThreads), 0, s, q.part,
                            q.groups, dq_gain, k.part, k.groups, dk_gain, head_dim);
         SNACK_HIP(hipGetLastError());
     }
