@@ -40,6 +40,18 @@ __device__ inline void store_key(uint8_t* tile, int nb, int t, int b, int g, f32
     }
     if (g == 0) tile[2 * code_bytes(FMT, nb) + k_exp_at(nb, t, b)] = (uint8_t)s;
 }
+// Four features of a key, 4 f .. 4 f + 3; the eight lanes of a block are neighbours.
+template <int FMT>
+__device__ inline void store_key4(uint8_t* tile, int nb, int t, int f, f32x4 y)
+{
+    const uint32_t s = cache_exponent<FMT>(octet_max(abs_max4(y)));
+    const uint32_t lo = cache_encode2<FMT>(y.x, y.y, s), hi = cache_encode2<FMT>(y.z, y.w, s);
+    const int b = f >> 3, g = (f & 7) >> 1, second = f & 1;
+    uint8_t* at = tile + k_code_at(FMT, nb, t, b, g);
+    if constexpr (four_bits(FMT)) reinterpret_cast<uint16_t*>(at)[second] = (uint16_t)(lo | hi << 8);
+    else reinterpret_cast<uint32_t*>(at)[second] = lo | hi << 16;
+    if ((f & 7) == 0) tile[2 * code_bytes(FMT, nb) + k_exp_at(nb, t, b)] = (uint8_t)s;
+}
 // features 32 b + 4 g + 0..3 and 32 b + 16 + 4 g + 0..3 of a value
 template <int FMT>
 __device__ inline void store_value(uint8_t* tile, int nb, int t, int b, int g, f32x8 y)
@@ -77,7 +89,7 @@ __device__ inline f32x4 part4(const X* p, int left)
 }
 
 // Workgroups 0..gq-1: queries, then gk of keys, then those of values.
-template <int LPR, typename X, typename Y>
+template <int LPR, bool EVEN, typename X, typename Y>
 __global__ void __launch_bounds__(kThreads) qk_pass_kernel(QkPass a, CacheView c, int fmt, uint32_t gq, uint32_t gk)
 {
     uint32_t group = blockIdx.x;
@@ -107,13 +119,37 @@ __global__ void __launch_bounds__(kThreads) qk_pass_kernel(QkPass a, CacheView c
         else store_value<SNACK_E2M1>(tile, c.nb, t, b, g, y);
         return;
     }
+    // whole pairs on a lane: outputs always, keys for the cache where a block's lanes are then neighbours
+    if (!kept || a.key_pairs) {
+        const Spot8 at = find_spot8(lane, a.d, a.ro.r, a.ro.layout);
+        const Eight z = qk_pairs<LPR, EVEN>(p, at, lane, a.d, kind == 0 ? a.q_gain : a.k_gain, a.eps, a.inv_d, a.ro,
+                                      a.ro.table ? a.pos[token] : 0);
+        if (!kept) {
+            Y* to = (Y*)(kind == 0 ? a.yq : a.yk) + (int64_t)row * a.d;
+            if (live) {
+                put4(to + at.a, z.a, at.na);
+                put4(to + at.b, z.b, at.nb);
+            }
+            return;
+        }
+        if (!place || !at.turned) return;
+        uint8_t* tile = cache_tile(c, slot, (int)h);
+        const int t = (int)(slot & (kTile - 1)), fa = at.a >> 2, fb = at.b >> 2;
+        if (fmt == SNACK_INT8) {
+            store_key4<SNACK_INT8>(tile, c.nb, t, fa, z.a);
+            store_key4<SNACK_INT8>(tile, c.nb, t, fb, z.b);
+        } else if (fmt == SNACK_E4M3) {
+            store_key4<SNACK_E4M3>(tile, c.nb, t, fa, z.a);
+            store_key4<SNACK_E4M3>(tile, c.nb, t, fb, z.b);
+        } else {
+            store_key4<SNACK_E2M1>(tile, c.nb, t, fa, z.a);
+            store_key4<SNACK_E2M1>(tile, c.nb, t, fb, z.b);
+        }
+        return;
+    }
     const f64x8 z = qk_value<LPR>(p, f0, a.d, kind == 0 ? a.q_gain : a.k_gain, a.eps, a.inv_d, a.ro,
                                   a.ro.table ? a.pos[token] : 0);
     const f32x8 y = __builtin_convertvector(z, f32x8);
-    if (!kept) {
-        if (live) store8((Y*)(kind == 0 ? a.yq : a.yk) + (int64_t)row * a.d + f0, y, a.d - f0);
-        return;
-    }
     const int b = lane >> 2, g = lane & 3;
     if (!place || b >= c.nb) return;
     uint8_t* tile = cache_tile(c, slot, (int)h);
@@ -237,13 +273,14 @@ read_kernel(CacheView c, const int64_t* __restrict__ slots, FastDiv heads, uint3
 }
 
 template <typename F>
-void with_lanes(int d, F f)
+void with_lanes(int lanes, F f)
 {
-    switch (head_lanes(d)) {
+    switch (lanes) {
     case 4: f(std::integral_constant<int, 4>{}); break;
     case 8: f(std::integral_constant<int, 8>{}); break;
     case 16: f(std::integral_constant<int, 16>{}); break;
-    default: f(std::integral_constant<int, 32>{}); break;
+    case 32: f(std::integral_constant<int, 32>{}); break;
+    default: f(std::integral_constant<int, 64>{}); break;
     }
 }
 
@@ -283,13 +320,21 @@ snack_status qk_pass(const QkPass& a, const CacheView* cache, int cache_fmt, int
     b.inv_d = 1.0 / a.d;
     CacheView c{};
     if (cache) c = *cache;
-    const uint32_t per = kThreads / head_lanes(a.d);
+    // heads of whole blocks, half of each turning with the other: the key path of whole pairs
+    b.key_pairs = a.ro.table && a.ro.layout == SNACK_ROPE_HALF && a.ro.r % kCkptBlock == 0 && 2 * a.ro.r == a.d &&
+                  cache_blocks(a.d) * kCkptBlock == a.d;
+    const int hl = head_lanes(a.d), pl = pair_lanes(a.d, a.ro.r), lanes = hl > pl ? hl : pl;
+    const uint32_t per = kThreads / lanes;
     const uint32_t gq = (a.q.rows + per - 1) / per, gk = (a.k.rows + per - 1) / per, gv = (a.v.rows + per - 1) / per;
-    with_lanes(a.d, [&](auto lanes) {
-        constexpr int LPR = decltype(lanes)::value;
-        const auto k = x_fmt == SNACK_F32
-                           ? y_fmt == SNACK_F32 ? qk_pass_kernel<LPR, float, float> : qk_pass_kernel<LPR, float, uint16_t>
-                           : y_fmt == SNACK_F32 ? qk_pass_kernel<LPR, uint16_t, float> : qk_pass_kernel<LPR, uint16_t, uint16_t>;
+    with_lanes(lanes, [&](auto n) {
+        constexpr int LPR = decltype(n)::value;
+        auto pick = [&](auto even) {
+            constexpr bool EVEN = decltype(even)::value;
+            if (x_fmt == SNACK_F32)
+                return y_fmt == SNACK_F32 ? qk_pass_kernel<LPR, EVEN, float, float> : qk_pass_kernel<LPR, EVEN, float, uint16_t>;
+            return y_fmt == SNACK_F32 ? qk_pass_kernel<LPR, EVEN, uint16_t, float> : qk_pass_kernel<LPR, EVEN, uint16_t, uint16_t>;
+        };
+        const auto k = even_lanes(a.d, a.ro.r) ? pick(std::true_type{}) : pick(std::false_type{});
         hipLaunchKernelGGL(k, dim3(gq + gk + gv), dim3(kThreads), 0, s, b, c, cache_fmt, gq, gk);
     });
     SNACK_HIP(hipGetLastError());
@@ -384,7 +429,7 @@ extern "C" snack_status snack_cache_read(const snack_cache* cache, const int64_t
     make_cache_view(cache, &c);
     const uint32_t per = kThreads / head_lanes(c.d), groups = (h.rows + per - 1) / per;
     const uint32_t gk = K ? groups : 0, gv = V ? groups : 0;
-    with_lanes(c.d, [&](auto lanes) {
+    with_lanes(head_lanes(c.d), [&](auto lanes) {
         constexpr int LPR = decltype(lanes)::value;
         auto launch = [&](auto fmt) {
             constexpr int FMT = decltype(fmt)::value;

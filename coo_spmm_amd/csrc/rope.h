@@ -211,9 +211,12 @@ __device__ inline Spot8 find_spot8(int lane, int d, int r, int layout)
         s.b = s.a + 4;
         s.na = max(0, min(4, end - s.a));
         s.nb = max(0, min(4, end - s.b));
+        if (s.na == 0) s.a = s.b = 0;    // a lane without features: its loads stay within the head
     }
     return s;
 }
+// whether every lane has eight features or none (EVEN below): no four that lacks some, none to move into place
+inline bool even_lanes(int d, int r) { return r % 4 == 0 && (d - 2 * r) % 8 == 0; }
 inline int pair_lanes(int d, int r)
 {
     const int n = (r + 3) / 4 + (d - 2 * r + 7) / 8;
@@ -227,10 +230,14 @@ __device__ inline f32x4 raw4(const uint16_t* p)
     const u16x4u h = *reinterpret_cast<const u16x4u*>(p);
     return f32x4{bf16_value(h.x), bf16_value(h.y), bf16_value(h.z), bf16_value(h.w)};
 }
-template <typename X>
+template <bool EVEN, typename X>
 __device__ inline f32x4 take4(const X* __restrict__ p, int i, int n, int m)
 {
     f32x4 v = {0, 0, 0, 0};
+    if constexpr (EVEN) {
+        v = raw4(p + i);
+        return m > 0 ? v : f32x4{0, 0, 0, 0};
+    }
     if (n < 4) {
 #pragma unroll
         for (int k = 0; k < 3; ++k)
@@ -242,10 +249,10 @@ __device__ inline f32x4 take4(const X* __restrict__ p, int i, int n, int m)
     if (over > 0) v = f32x4{over == 1 ? v.y : over == 2 ? v.z : v.w, over == 1 ? v.z : v.w, v.w, 0.0f};
     return f32x4{m > 0 ? v.x : 0.0f, m > 1 ? v.y : 0.0f, m > 2 ? v.z : 0.0f, m > 3 ? v.w : 0.0f};
 }
-template <typename X>
+template <bool EVEN, typename X>
 __device__ inline Eight take8(const X* __restrict__ p, const Spot8& s, int d)
 {
-    return Eight{take4(p, s.a, d, s.na), take4(p, s.b, d, s.nb)};
+    return Eight{take4<EVEN>(p, s.a, d, s.na), take4<EVEN>(p, s.b, d, s.nb)};
 }
 __device__ inline void put4(float* __restrict__ p, f32x4 v, int m)
 {
@@ -267,12 +274,13 @@ __device__ inline void put4(uint16_t* __restrict__ p, f32x4 v, int m)
 struct Angles {
     f32x4 c, s;
 };
+template <bool EVEN>
 __device__ inline Angles take_angles(const Rotation& ro, int pos, int lane, bool turned)
 {
     const bool ok = (uint32_t)pos < ro.positions;
     const float* row = ro.table + (int64_t)(ok ? pos : 0) * (2 * ro.r);
     const int i = turned ? 4 * lane : 0, m = turned ? min(4, ro.r - i) : 0;
-    Angles t{take4(row, i, ro.r, m), take4(row + ro.r, i, ro.r, m)};
+    Angles t{take4<EVEN>(row, i, ro.r, m), take4<EVEN>(row + ro.r, i, ro.r, m)};
     const float one = ok ? 1.0f : __builtin_nanf("");
     if (!turned || !ok) t.c = f32x4{one, one, one, one};
     return t;
@@ -333,6 +341,63 @@ __device__ inline f64x8 qk_value(const X* __restrict__ p, int f0, int d, const f
     return z;
 }
 
+// The same on lanes that hold whole pairs (find_spot8): everything is loaded before the first of it is waited for.
+struct Eight64 {
+    double a[4], b[4];
+};
+template <int LPR, bool EVEN, typename X>
+__device__ inline Eight qk_pairs(const X* __restrict__ p, const Spot8& at, int lane, int d, const float* __restrict__ gain,
+                                 double eps, double inv_d, const Rotation& ro, int pos)
+{
+    const Eight x = take8<EVEN>(p, at, d);
+    Eight g{{1, 1, 1, 1}, {1, 1, 1, 1}};
+    if (gain) g = take8<EVEN>(gain, at, d);
+    Angles t{{1, 1, 1, 1}, {0, 0, 0, 0}};
+    if (ro.table) t = take_angles<EVEN>(ro, pos, lane, at.turned);
+    Eight64 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y.a[i] = x.a[i];
+        y.b[i] = x.b[i];
+    }
+    if (gain) {
+        double ss = 0.0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = fma(y.b[i], y.b[i], fma(y.a[i], y.a[i], ss));
+        const double v = fma(lanes_sum<LPR>(ss), inv_d, eps);
+        // an infinity among the features: their quotients are 0, and NaN where they are infinite
+        const double rstd = v < __builtin_inf() ? rsqrt64(v) : v == v ? 0.0 : v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y.a[i] *= rstd * g.a[i];
+            y.b[i] *= rstd * g.b[i];
+        }
+    }
+    Eight z;
+    if (at.turned && ro.layout == SNACK_ROPE_HALF) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z.a[i] = (float)fma(-y.b[i], (double)t.s[i], y.a[i] * t.c[i]);
+            z.b[i] = (float)fma(y.a[i], (double)t.s[i], y.b[i] * t.c[i]);
+        }
+    } else if (at.turned) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            z.a[2 * i] = (float)fma(-y.a[2 * i + 1], (double)t.s[i], y.a[2 * i] * t.c[i]);
+            z.a[2 * i + 1] = (float)fma(y.a[2 * i], (double)t.s[i], y.a[2 * i + 1] * t.c[i]);
+            z.b[2 * i] = (float)fma(-y.b[2 * i + 1], (double)t.s[2 + i], y.b[2 * i] * t.c[2 + i]);
+            z.b[2 * i + 1] = (float)fma(y.b[2 * i], (double)t.s[2 + i], y.b[2 * i + 1] * t.c[2 + i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z.a[i] = (float)(y.a[i] * t.c[i]);
+            z.b[i] = (float)(y.b[i] * t.c[i]);
+        }
+    }
+    return z;
+}
+
 // lanes of a head of d features
 inline int head_lanes(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
@@ -356,6 +421,7 @@ struct QkPass {
     const float *q_gain, *k_gain;
     double eps, inv_d;
     void *yq, *yk;
+    bool key_pairs;     // set by qk_pass
 };
 snack_status qk_pass(const QkPass& a, const CacheView* cache, int cache_fmt, int x_fmt, int y_fmt, int kclass,
                      hipStream_t s);

@@ -18,7 +18,8 @@ namespace snack {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxGroups = 2048;    // workgroups (and partial rows) of a gradient at most
+constexpr int kMaxGroups = 1280;    // workgroups (and partial rows) of a gradient at most: five a compute unit, all at once
+                                    // (2048: 71 against 62 us at 9001 tokens of 24 heads of 80)
 constexpr int kSumThreads = 1024, kSumCols = 8;
 
 __global__ void __launch_bounds__(kThreads) table_kernel(float* __restrict__ T, uint32_t total, FastDiv by_r,
@@ -49,7 +50,7 @@ struct BwdPart {
     uint32_t run;        // heads (rows) of a workgroup
 };
 
-template <int LPR, typename X, typename Y>
+template <int LPR, bool EVEN, typename X, typename Y>
 __global__ void __launch_bounds__(kThreads)
 qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rotation ro, double eps, double inv_d)
 {
@@ -62,7 +63,7 @@ qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rota
     const Spot8 at8 = find_spot8(lane, d, ro.r, ro.layout);
     const uint32_t first = group * a.run, last = min(a.x.rows, first + a.run);
     Eight gain{{0, 0, 0, 0}, {0, 0, 0, 0}}, dg = gain;
-    if (a.gain) gain = take8(a.gain, at8, d);
+    if (a.gain) gain = take8<EVEN>(a.gain, at8, d);
     // whole wavefronts stay in the loop: the sums over lanes take every lane
     for (uint32_t at = first; at < last; at += kRows) {
         const uint32_t row = at + threadIdx.x / LPR;
@@ -70,11 +71,11 @@ qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rota
         const uint32_t rr = live ? row : last - 1;
         const uint32_t token = fast_quot(a.x.heads, rr), h = rr - token * a.x.heads.d;
         const int p = ro.table ? pos[token] : 0;
-        Eight dy = take8((const Y*)a.g.p + (int64_t)token * a.g.row + (int64_t)h * a.g.head, at8, d);
+        Eight dy = take8<EVEN>((const Y*)a.g.p + (int64_t)token * a.g.row + (int64_t)h * a.g.head, at8, d);
         Eight x{{0, 0, 0, 0}, {0, 0, 0, 0}};
-        if (a.gain) x = take8((const X*)a.x.p + (int64_t)token * a.x.row + (int64_t)h * a.x.head, at8, d);
+        if (a.gain) x = take8<EVEN>((const X*)a.x.p + (int64_t)token * a.x.row + (int64_t)h * a.x.head, at8, d);
         if (ro.table) {
-            const Angles t = take_angles(ro, p, lane, at8.turned);
+            const Angles t = take_angles<EVEN>(ro, p, lane, at8.turned);
             const Eight g = dy;
             if (ro.layout == SNACK_ROPE_HALF || !at8.turned) {
                 dy.a = g.a * t.c + g.b * t.s;
@@ -315,8 +316,11 @@ extern "C" snack_status snack_qk_rope_bwd(const void* Q, int64_t q_row, int64_t 
     const unsigned groups = q.groups + k.groups;
     if (groups) {
         auto launch = [&](auto lanes, auto x, auto y) {
-            hipLaunchKernelGGL((qk_bwd_kernel<decltype(lanes)::value, decltype(x), decltype(y)>), dim3(groups),
-                               dim3(kThreads), 0, s, q, k, head_dim, pos, ro, (double)eps, 1.0 / head_dim);
+            constexpr int LPR = decltype(lanes)::value;
+            const auto kernel = even_lanes(head_dim, ro.r) ? qk_bwd_kernel<LPR, true, decltype(x), decltype(y)>
+                                                           : qk_bwd_kernel<LPR, false, decltype(x), decltype(y)>;
+            hipLaunchKernelGGL(kernel, dim3(groups), dim3(kThreads), 0, s, q, k, head_dim, pos, ro, (double)eps,
+                               1.0 / head_dim);
         };
         auto types = [&](auto lanes) {
             if (x_fmt == SNACK_F32) {
