@@ -88,7 +88,10 @@ __device__ inline f32x4 part4(const X* p, int left)
     return v;
 }
 
-// Workgroups 0..gq-1: queries, then gk of keys, then those of values.
+// Workgroups 0..gq-1: queries, then gk of keys, then those of values.  Measured: 8192 tokens of 32 query and 8 key heads
+// of 128, fp32 to bf16, 254 MB in 59 us (4.3 TB/s); 8192 tokens of 12 heads of 64 into an int8 cache, 126 MB in 44 us (the
+// values' codes go out two bytes at a time, into lines that eight tokens fill); one token 3.4 us (a launch).  EVEN spares
+// the selects that move a partial four into place: 59 against 84 us.
 template <int LPR, bool EVEN, typename X, typename Y>
 __global__ void __launch_bounds__(kThreads) qk_pass_kernel(QkPass a, CacheView c, int fmt, uint32_t gq, uint32_t gk)
 {

@@ -86,7 +86,7 @@ class Case:
 CASES = [([1], [1], 1, 1, 1, 32), ([5], [1], 12, 12, 64, 64), ([32, 33, 31], [1, 1, 1], 8, 2, 128, 32),
          ([1000], [1], 12, 12, 64, 64), ([257, 3, 700], [1, 1, 1], 32, 2, 96, 96), ([64, 1], [4, 1], 15, 3, 80, 32),
          ([300, 40], [7, 40], 6, 3, 160, 64), ([97, 128, 5, 0], [17, 0, 5, 2], 4, 4, 200, 32), ([2100], [3], 16, 1, 256, 256),
-         ([129] * 5, [1] * 5, 5, 1, 33, 128), ([77, 20], [30, 3], 40, 2, 32, 32)]
+         ([129] * 5, [1] * 5, 5, 1, 33, 128), ([70, 300], [2, 1], 2, 2, 192, 64), ([77, 20], [30, 3], 40, 2, 32, 32)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -124,6 +124,20 @@ def test_long_context_is_split():
             c = Case(lens, [1] * len(lens), 4, 2, 64, fmt, 128, f"long/{len(lens)}")
             say("long", len(lens), fmt)
             c.check(c.run())
+
+
+@pytest.mark.parametrize("nq", [1, 20, 132])
+def test_more_units_than_workgroups(nq):
+    """Short and long sequences of every kind of block, more of them than workgroups, some without a query."""
+    rng = np.random.default_rng(nq)
+    n = {1: 180, 20: 150, 132: 70}[nq]
+    lens = [int(x) for x in rng.integers(1, 400, n)]
+    lens[5], lens[6], lens[7] = 1900, 0, 2
+    nqs = [nq] * n
+    nqs[9], nqs[10] = 0, 0
+    c = Case(lens, nqs, 4, 4, 32, A.E2M1, 32, f"units/{nq}")
+    say("units", nq)
+    c.check(c.run())
 
 
 def test_large_scores():
