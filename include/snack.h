@@ -587,7 +587,7 @@ snack_status snack_cache_read(const snack_cache* cache, const int64_t* slot, int
  * scale finite, above 0.  Sums, maxima and the softmax are held in fp32.
  * SNACK_F32: q and the softmax's terms enter the products exactly, as sums of three
  * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are rounded to bf16
- * (at most 16 queries a head: to two).
+ * (to the sum of two where a sequence has at most 16 queries a cache head on average).
  *   work  device scratch of snack_cache_attend_work bytes, 16-byte aligned, used
  *         within the call (SNACK_ERR_WORKSPACE when work_bytes is less).
  */
