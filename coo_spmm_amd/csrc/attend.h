@@ -227,8 +227,8 @@ __device__ inline Cursor find_block(const AttendArgs& a, const Schedule<THREADS>
     c.cost = c.tiles + unit_cost<ROWS>();
     return c;
 }
-// one sequence of a few blocks: every thread counts them all, without the two rounds through LDS (7.9 -> 6.5 us for a stream's
-// single token)
+// one sequence of a few blocks: every thread counts them all, without the two rounds through LDS (7.9 -> 6.5 us for
+// one token of a stream of 1000)
 template <int ROWS>
 __device__ inline bool few_blocks(const AttendArgs& a)
 {

@@ -161,7 +161,7 @@ def test_rising_maximum():
         c.check(c.run())
 
 
-@pytest.mark.parametrize("nq", [1, 3, 40])
+@pytest.mark.parametrize("nq", [1, 3, 40, 100])
 @pytest.mark.parametrize("fmt", FMTS)
 def test_what_is_not_seen_has_no_influence(fmt, nq):
     """NaN and infinities in keys and values that some queries see and others do not."""

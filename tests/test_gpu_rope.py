@@ -111,9 +111,9 @@ def test_backward(shape, layout):
             if not gains:
                 assert gg is None
                 continue
-            # a lane's heads one after the other (a workgroup of 256 threads takes 8 to 64 heads at once, and at least
-            # a fifth of 2048 workgroups share them), its workgroup's, then 64 bits; 5 of each term
-            chain = -(-t * h // (8 * 400)) + 64 + 6
+            # a lane's heads one after the other (a workgroup of 256 threads takes 4 to 64 heads at once, and at least
+            # a sixth of 1280 workgroups share them out), its workgroup's 64, then 64 bits; 6 of each term
+            chain = -(-t * h // (4 * 200)) + 64 + 6
             _close(host(gg), dg, chain * U32 * ag, "dgain")
     if rot:     # queries alone give the same
         (q, k, tab, pos, gq, gk, dq, dk), got = _bwd_case(shape, layout, "f32", "f32", True, f"ropeb/{shape}")
@@ -251,3 +251,33 @@ def test_captured_gradient_beside_an_eager_one():
         eager = L.qk_rope_bwd(q, k, pos, dq, dk, rope, gq, gk)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, eager)), i
+
+
+def test_past_2_31_values():
+    """Offsets past 32 bits: a thousand copies of the same tokens give a thousand times the same rows."""
+    import torch
+    L = lib()
+    t, h, d, n = 70, 128, 256, 1000
+    base = dev(normal((t, h, d), "rope/large").astype(np.float32)).to(torch.bfloat16)
+    x = base.repeat(n, 1, 1)
+    assert x.numel() > 2 ** 31
+    pos = (torch.arange(t * n, device="cuda") % t).to(torch.int32)
+    rope = L.RopeTable.make(t, 64)
+    gain = torch.rand(d, device="cuda") + 0.5
+    say("past 2^31")
+    y = L.qk_rope_fwd(x, None, pos, rope, gain)[0].view(n, t, h, d)
+    want = L.qk_rope_fwd(base, None, pos[:t], rope, gain)[0]
+    assert all(torch.equal(y[i], want) for i in (0, n // 2, n - 2, n - 1))
+    del y
+    dx, _, dg, _ = L.qk_rope_bwd(x, None, pos, x, None, rope, gain)
+    wx, _, wg, _ = L.qk_rope_bwd(base, None, pos[:t], base, None, rope, gain)
+    dx = dx.view(n, t, h, d)
+    assert all(torch.equal(dx[i], wx) for i in (0, n // 2, n - 2, n - 1))
+    # sums of n times as many terms, each side within its own chain of roundings of the terms' magnitudes (above): heads
+    # of a lane (4 to a workgroup of 256 at 64 lanes, 8 at 32; 1280 workgroups), its workgroup's, 6 of each term
+    dq = host(base.float())
+    ag = A.qk_bwd(dq, dq, host(gain), 1e-6, A.table(t, 64), np.arange(t), A.HALF)[3]
+    chain = -(-t * n * h // (4 * 1280)) + 64 + 6
+    _close(host(dg), n * host(wg).astype(np.float64), 2 * n * chain * U32 * ag, "dgain")
+    del x, dx
+    torch.cuda.empty_cache()
