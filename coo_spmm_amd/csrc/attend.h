@@ -631,9 +631,10 @@ __device__ inline void store_out(void* out, int64_t at, int d, int dims, f32x4 v
     }
 }
 
-// The pieces of a unit (blockIdx.x: the unit, or the workgroup that started it), joined: 16 queries (blockIdx.y).  WIDE (few blocks of many pieces each): 16 features (blockIdx.z), the wavefronts sharing the pieces out;
-// else every wavefront some of the features, over all pieces.  Maxima and sums first, so that the pieces' outputs are
-// then added up with known weights and all on their way at once.
+// The pieces of a unit (blockIdx.x: the unit, or the workgroup that started it), joined: 16 queries (blockIdx.y).  WIDE
+// (few units of many pieces each): 16 features (blockIdx.z), the wavefronts sharing the pieces out; else every wavefront
+// some of the features, over all pieces.  A chain of three loads bounds it: the unit, its pieces' maxima, sums and
+// outputs all at once, the result (4 to 5 us with its launch; 40 MB of pieces in 9.5 us).
 template <int QT, int ROWS, bool WIDE>
 __global__ void __launch_bounds__(kAttendThreads) attend_join_kernel(AttendArgs a)
 {

@@ -1,8 +1,10 @@
 // rope.h -- one head of one token on a group of lanes: its norm and its rotation.
 //
-// Eight consecutive features a lane (16 or 32 bytes of memory), LPR lanes a head:
-// the power of two that covers its blocks of 32 features, so a block is four
-// neighbouring lanes.
+// LPR lanes a head, eight features each (16 or 32 bytes of memory), in one of two
+// ways.  Eight in a row: a block of 32 features is four neighbouring lanes, as the
+// cache takes keys and values.  Whole pairs of the rotation (find_spot8): nothing is
+// read twice; for what is written as it is, and for keys where eight neighbouring
+// lanes then hold a block.
 #pragma once
 
 #include "ckpt.h"
@@ -111,14 +113,12 @@ __device__ inline void store8(uint16_t* __restrict__ p, f32x8 v, int left)
     }
 }
 
-// What turns a lane's features f0..f0+7: feature i becomes c[i] x[i] + s[i] x[partner], sin with the sign of
-// the forward direction (back: of the transposed one).  cos is 1 and sin 0 past the rotated features.
-// `base` is where the head's features start; other(f) gives feature f of it as the caller wants it.
-// A lane whose features all lie on one side of the pairs takes its partners as a vector (other8).
+// What turns a lane's features f0..f0+7: feature i becomes c[i] x[i] + s[i] x[partner], sin with its sign; cos is 1
+// and sin 0 past the rotated features.
 struct Turn {
     f32x8 c, s;
 };
-__device__ inline Turn load_turn(const Rotation& ro, int pos, int f0, bool back)
+__device__ inline Turn load_turn(const Rotation& ro, int pos, int f0)
 {
     Turn t;
     const bool ok = (uint32_t)pos < ro.positions;
@@ -136,7 +136,6 @@ __device__ inline Turn load_turn(const Rotation& ro, int pos, int f0, bool back)
                 s[i] = i0 + i < ro.r ? row[ro.r + i0 + i] : 0.0f;
             }
         }
-        if (back) s = -s;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             t.c[2 * i] = t.c[2 * i + 1] = c[i];
@@ -148,7 +147,7 @@ __device__ inline Turn load_turn(const Rotation& ro, int pos, int f0, bool back)
         const int i0 = second ? f0 - ro.r : f0;
         t.c = load8(row + i0, 8);
         t.s = load8(row + ro.r + i0, 8);
-        if (second == back) t.s = -t.s;
+        if (!second) t.s = -t.s;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -156,7 +155,7 @@ __device__ inline Turn load_turn(const Rotation& ro, int pos, int f0, bool back)
             const bool in = f < 2 * ro.r;
             t.c[i] = in ? row[j] : 1.0f;
             const float s = in ? row[ro.r + j] : 0.0f;
-            t.s[i] = (f >= ro.r) == back ? -s : s;
+            t.s[i] = f < ro.r ? -s : s;
         }
     }
     if (!ok) {
@@ -320,7 +319,7 @@ __device__ inline f64x8 qk_value(const X* __restrict__ p, int f0, int d, const f
         if (ro.table && (uint32_t)pos >= ro.positions) y *= __builtin_nan("");
         return y;
     }
-    const Turn t = load_turn(ro, pos, f0, false);
+    const Turn t = load_turn(ro, pos, f0);
     f64x8 o;
     if (ro.layout == SNACK_ROPE_PAIRS) {
         o = swap_pairs(y);
