@@ -23,7 +23,7 @@
 // Measured (both launches): 64 streams of 256 to 4096 tokens, 8 cache heads of 128 in
 // 4 bits, 154 MB, fp32 queries 51 us; one of 131072 tokens, 143 MB, bf16 queries 39 us
 // (a copy's rate would be 30 and 28); 512 queries over 8192 tokens, int8, 67 GFLOP,
-// bf16 119 us; four prompts of 1024 tokens, 12 heads of 64, fp32 (three products
+// bf16 (two products with V) 132 us; four prompts of 1024 tokens, 12 heads of 64, fp32 (three products
 // each) 59 us.
 #pragma once
 

@@ -222,9 +222,11 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
 // instructions and of the exponentials and conversions beside them, so a tile is decoded once for all wavefronts: half
 // of them take a share of K, half one of V, and leave operands in LDS, in the order in which lanes read them (16
 // bytes a lane in a row: no bank conflicts).  Two buffers: while one tile is multiplied, the next is decoded and the
-// one after it is on its way from memory, with one barrier a tile.  bf16 queries: probabilities are rounded to bf16
-// once, which the output's own rounding hides (each is off by at most 2^-8 of itself, at random), and their sum is
-// one more row of the second product.
+// one after it is on its way from memory, with one barrier a tile.  bf16 queries: a probability is the sum of two bf16
+// numbers, off by at most 2^-16 of itself, as in the kernel of few queries, so that a query's result does not depend on
+// which kernel the call's other sequences put it into; the sum of the probabilities is one more row of the second
+// product.  (512 queries over 8192 tokens: 132 us, with one bf16 number 109; but where values cancel that one's error is as
+// large as the output's own rounding, and the error against 64 bits 2.2e-3 against 1.7e-3.)
 //
 // A share is units of the words of one V block, or of two neighbouring blocks of one half of K, which are as many:
 // wavefront w of the first half has half w % 2 and the units w / 2, w / 2 + W / 4, ..., one of the second the V blocks
@@ -283,7 +285,7 @@ template <int FMT, int NB, int QT, int W, int NT>
 __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_kernel(AttendArgs a)
 {
     constexpr int THREADS = W * kWave, ROWS = 16 * W * NT;
-    constexpr int QP = QT == SNACK_F32 ? 3 : 1, PP = QT == SNACK_F32 ? 3 : 1;
+    constexpr int QP = QT == SNACK_F32 ? 3 : 1, PP = QT == SNACK_F32 ? 3 : 2;
     constexpr bool kSumRow = QT != SNACK_F32;
     using Q = typename QType<QT>::T;
     using S = Share<FMT, NB, W>;
@@ -515,8 +517,10 @@ __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_k
                 }
                 if constexpr (kSumRow) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        lsum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n][0], lsum[n], 0, 0, 0);
+                    for (int j = PP - 1; j >= 0; --j)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            lsum[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n][j], lsum[n], 0, 0, 0);
                 }
 #pragma unroll
                 for (int i = 0; i < 2 * NB; ++i) {

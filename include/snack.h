@@ -586,8 +586,8 @@ snack_status snack_cache_read(const snack_cache* cache, const int64_t* slot, int
  * that would read past the table's width or a page the cache does not have gets NaN.
  * scale finite, above 0.  Sums, maxima and the softmax are held in fp32.
  * SNACK_F32: q and the softmax's terms enter the products exactly, as sums of three
- * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are rounded to bf16
- * (to the sum of two where a sequence has at most 16 queries a cache head on average).
+ * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are sums of two bf16
+ * numbers (off by at most 2^-16 of themselves).
  *   work  device scratch of snack_cache_attend_work bytes, 16-byte aligned, used
  *         within the call (SNACK_ERR_WORKSPACE when work_bytes is less).
  */

@@ -362,3 +362,21 @@ def test_served_tokens_equal_the_whole_sequence(fmt):
         tol = np.expm1(2 * ((6 * 32 * 2 * U32 * 2 + 8 * U32) * terms + 20 * U32) + 150 * 2 * U32)[..., None] * mag
         one = np.concatenate(got[b])
         assert (np.abs(one - want) <= tol).all() and (np.abs(full[m[0] * b:m[0] * b + m[b]] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("nq", [1, 5, 24, 70])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_bf16_queries_lose_no_more_than_the_output_does(fmt, nq):
+    """Blocks of 16, 64 and 256 queries of a cache head (4, 20, 96 and 280 of them here): a probability is the sum of two
+    bf16 numbers in each.  The first is cut off, so the rest is below 2^(e - 7) of a probability from 2^e on, and its own
+    rounding, half a step of 8 bits, below 2^(e - 16).  Beside that and fp32's sums only the output is rounded."""
+    for d, causal in ((64, True), (128, False)):
+        c = Case([600], [nq], 8, 2, d, fmt, 64, f"bf16/{nq}", "bf16")
+        say("bf16 queries", fmt, nq, d)
+        got, q = host(c.run(causal).float()), host(c.q.float())
+        limits = [600 - nq + i if causal else 599 for i in range(nq)]
+        want, mag, terms, top = A.attend(q, c.k[0], c.v[0], d ** -0.5, limits)
+        tol = A.attend_tol(600, d, mag, terms, top, 2.0 ** -16)
+        tol = U16 * (np.abs(want) + tol) + tol + 2.0 ** -133
+        bad = ~(np.abs(got - want) <= tol)
+        assert not bad.any(), f"{int(bad.sum())} of {bad.size} off, at most by {np.max(np.abs(got - want) / tol)} of the tolerance"
