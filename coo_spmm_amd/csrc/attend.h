@@ -53,6 +53,7 @@ struct AttendArgs {
     const int32_t* lens;
     const int32_t* starts;
     int32_t sequences, per, tokens;   // per: tokens of a sequence where starts is null
+    int32_t most_blocks;              // blocks of queries of a cache head that ascending starts can give
     int32_t hq;
     FastDiv by_group;                 // query heads of a cache head
     float scale_log2;                 // scale * log2(e)
@@ -203,7 +204,7 @@ __device__ inline int last_at_most(const T* v, T x)
 // tiles.
 template <int THREADS>
 struct Schedule {
-    int32_t seqs[THREADS + THREADS / kWave];   // blocks before a thread's run of sequences
+    int64_t seqs[THREADS + THREADS / kWave];   // blocks before a thread's run of sequences
     int64_t work[THREADS + THREADS / kWave];   // tiles before a thread's run of blocks
 };
 template <int THREADS, int ROWS>
@@ -214,10 +215,10 @@ __device__ inline Cursor find_block(const AttendArgs& a, const Schedule<THREADS>
         const int32_t blocks = (int32_t)(((uint32_t)a.per * a.by_group.d + ROWS - 1) / ROWS);
         set_cursor<ROWS>(a, c, i / blocks, i % blocks);
     } else {
-        const int th = last_at_most<THREADS>(l.seqs, i);
+        const int th = last_at_most<THREADS>(l.seqs, (int64_t)i);
         const int32_t run = (a.sequences + THREADS - 1) / THREADS;
         set_cursor<ROWS>(a, c, th * run, 0);
-        c.k = i - l.seqs[th];
+        c.k = (int32_t)(i - l.seqs[th]);
         while (c.k >= c.blocks) {
             const int32_t k = c.k - c.blocks;
             set_cursor<ROWS>(a, c, c.b + 1, k);
@@ -234,7 +235,8 @@ __device__ inline bool few_blocks(const AttendArgs& a)
 {
     return !a.starts && a.sequences == 1 && (uint32_t)a.per * a.by_group.d <= 8 * ROWS;
 }
-// all tiles, and the runs' sums in l
+// all tiles, and the runs' sums in l.  Starts that do not ascend may claim tokens many times over: more blocks than
+// there is room for in the pieces' list, or than 32 bits hold.  Such a call has no work, in every workgroup.
 template <int THREADS, int ROWS>
 __device__ inline int64_t count_work(const AttendArgs& a, Schedule<THREADS>& l, int32_t* all_blocks)
 {
@@ -252,9 +254,14 @@ __device__ inline int64_t count_work(const AttendArgs& a, Schedule<THREADS>& l, 
     } else {
         const int32_t run = (a.sequences + THREADS - 1) / THREADS;
         const int32_t b0 = min((int32_t)threadIdx.x * run, a.sequences), b1 = min(b0 + run, a.sequences);
-        int32_t n = 0;
+        int64_t n = 0, all;
         for (int32_t b = b0; b < b1; ++b) n += seq_blocks<ROWS>(a, get_seq(a, b));
-        group_scan<THREADS>(n, l.seqs, &blocks);
+        group_scan<THREADS>(n, l.seqs, &all);
+        if (all > a.most_blocks) {
+            *all_blocks = 0;
+            return 0;
+        }
+        blocks = (int32_t)all;
     }
     *all_blocks = blocks;
     const int32_t run = (blocks + THREADS - 1) / THREADS;

@@ -121,6 +121,7 @@ extern "C" snack_status snack_cache_attend(const snack_cache* cache, const void*
     a.sequences = sequences;
     a.per = starts ? 0 : (int32_t)(tokens / sequences);
     a.tokens = (int32_t)tokens;
+    a.most_blocks = (int32_t)(plan.units / cache->heads);
     a.hq = q_heads;
     a.by_group = fast_div((uint32_t)group);
     a.scale_log2 = (float)((double)scale * 1.4426950408889634);

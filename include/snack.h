@@ -525,7 +525,9 @@ snack_status snack_qk_rope_bwd(const void* Q, int64_t q_row, int64_t q_head, int
  * each: sequence b has tokens starts[b] .. starts[b + 1] - 1 (device
  * int32[sequences + 1], ascending; NULL: tokens / sequences each, which must then
  * divide), the last of the lens[b] (device int32[sequences]) that the cache holds
- * of it with them.  Tokens outside of starts belong to no sequence.
+ * of it with them.  Tokens outside of starts belong to no sequence.  Starts that do
+ * not ascend cause no access outside of the arrays; which results of such a call are
+ * written is not specified.
  */
 typedef struct snack_cache {
     uint8_t* data;

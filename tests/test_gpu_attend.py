@@ -380,3 +380,41 @@ def test_bf16_queries_lose_no_more_than_the_output_does(fmt, nq):
         tol = U16 * (np.abs(want) + tol) + tol + 2.0 ** -133
         bad = ~(np.abs(got - want) <= tol)
         assert not bad.any(), f"{int(bad.sum())} of {bad.size} off, at most by {np.max(np.abs(got - want) / tol)} of the tolerance"
+
+
+# tokens, query heads, cache heads, sequences: blocks of 64, 16 and 256 queries; more blocks than 32 bits hold
+@pytest.mark.parametrize("tokens,hq,hk,n", [(200, 32, 8, 14), (1024, 1, 1, 64), (1024, 4, 1, 9), (1 << 16, 8, 1, (1 << 17) + 1)])
+def test_starts_that_claim_tokens_many_times(tokens, hq, hk, n):
+    """Starts 0, T, 0, T, ... claim all tokens over and over: more units than the workspace has entries for.  Nothing
+    behind it is written, nor any result; the same call with starts that ascend, in the same workspace, is right."""
+    import torch
+    L = lib()
+    d, page = 32, 32
+    c = L.KVCache(2, hk, d, A.INT8, page=page)
+    k, v = (normal((64, hk, d), "claims/" + s).astype(np.float32) for s in "kv")
+    c.write(dev(k), dev(v), dev(np.arange(64)))
+    q = dev(normal((min(tokens, 1024), hq, d), "claims/q").astype(np.float32)).repeat(-(-tokens // 1024), 1, 1)
+    assert q.shape[0] == tokens
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda").repeat(n, 1)
+    lens = torch.full((n,), 50, dtype=torch.int32, device="cuda")
+    starts = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    starts[1::2] = tokens
+    nbytes, guard = L.snack_cache_attend_work(c._ref, hq, tokens, n), 1 << 20
+    room = torch.full((nbytes + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((tokens, hq, d), 7.5, device="cuda")
+
+    def run(s):
+        L.snack_cache_attend(c._ref, q, L.F32, table, lens, s, d ** -0.5, False, out, room[:nbytes])
+        torch.cuda.synchronize()
+        assert (room[nbytes:] == 0xA5).all()
+    say("claims", tokens, hq, hk, n)
+    run(starts)
+    assert (out == 7.5).all()
+    starts[:] = tokens
+    starts[0] = 0
+    run(starts)
+    rows = np.concatenate([np.arange(32) + 32, np.arange(18)])
+    want, mag, terms, top = A.attend(host(q[:3]), A.grid(k, A.INT8)[rows], A.grid(v, A.INT8)[rows], d ** -0.5, [49] * 3)
+    assert (np.abs(host(out[:3]) - want) <= A.attend_tol(50, d, mag, terms, top) + 1e-37).all()
+    step = min(tokens, 1024)
+    assert all(torch.equal(out[i:i + step], out[:step]) for i in range(step, tokens, step))
