@@ -320,6 +320,10 @@ __device__ inline float query_sum(float x)
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// A query's running maximum after scores of at most `top`.  Each query decides by itself: raised along with another of
+// its wavefront, it would be rounded otherwise, and a token that only the other sees would show in its result.
+__device__ inline float raised(float m, float top) { return top > m + kRaise ? top : m; }
+
 // the largest of eight, a NaN left out: the median of two numbers and infinity is their maximum, and takes its
 // operands as they are (the library's maximum first quiets what could be a signalling NaN: four instructions more)
 __device__ inline float max8(const float* x)

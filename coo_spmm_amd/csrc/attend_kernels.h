@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
             }
             const float top = max8(x) * a.scale_log2;
             if (__ballot(top > mc + kRaise)) {
-                const float m = fmaxf(mc, query_max(top));
+                const float m = raised(mc, query_max(top));
                 const float f = m == mc ? 1.0f : __builtin_amdgcn_exp2f(mc - m);
 #pragma unroll
                 for (int i = 0; i < 2 * NB; ++i) o[i] *= f;
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_k
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     if (__ballot(top[n] > mc[n] + kRaise)) {
-                        const float m = fmaxf(mc[n], query_max(top[n]));
+                        const float m = raised(mc[n], query_max(top[n]));
                         const float f = m == mc[n] ? 1.0f : __builtin_amdgcn_exp2f(mc[n] - m);
 #pragma unroll
                         for (int i = 0; i < 2 * NB; ++i) o[n][i] *= f;

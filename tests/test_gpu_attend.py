@@ -418,3 +418,22 @@ def test_starts_that_claim_tokens_many_times(tokens, hq, hk, n):
     assert (np.abs(host(out[:3]) - want) <= A.attend_tol(50, d, mag, terms, top) + 1e-37).all()
     step = min(tokens, 1024)
     assert all(torch.equal(out[i:i + step], out[:step]) for i in range(step, tokens, step))
+
+
+@pytest.mark.parametrize("nq", [3, 8, 40, 140])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_large_score_of_another_query_has_no_influence(fmt, nq):
+    """The newest token's key gives its own query, which alone sees it, a score far above all others: the queries before
+    it, in the same block, keep every bit."""
+    import torch
+    n, hq, hk, d = 200, 4, 2, 64
+    for qtype in ("f32", "bf16"):
+        c = Case([n], [nq], hq, hk, d, fmt, 32, f"another/{nq}", qtype)
+        outs = []
+        for size in (0.0, 20.0):
+            k = host(c.q.float())[-1:, ::hq // hk] * size
+            c.cache.write(dev(k), dev(np.ones((1, hk, d), np.float32)), dev(c.slots(0, n)[-1:]))
+            say("another", fmt, nq, qtype, size)
+            outs.append(c.run())
+        assert torch.equal(outs[0][:-1], outs[1][:-1])
+        assert not torch.equal(outs[0][-1], outs[1][-1])
