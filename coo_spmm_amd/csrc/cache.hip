@@ -12,6 +12,8 @@ namespace snack {
 namespace {
 
 constexpr int kThreads = 256;
+// Workgroups of a launch at most: HIP takes fewer than 2^32 threads.  What needs more is launched in pieces.
+constexpr uint32_t kLaunchGroups = 1u << 23;
 
 __device__ inline uint32_t abs_max8(f32x8 x)
 {
@@ -93,9 +95,9 @@ __device__ inline f32x4 part4(const X* p, int left)
 // values' codes go out two bytes at a time, into lines that eight tokens fill); one token 3.4 us (a launch).  EVEN spares
 // the selects that move a partial four into place: 59 against 84 us.
 template <int LPR, bool EVEN, typename X, typename Y>
-__global__ void __launch_bounds__(kThreads) qk_pass_kernel(QkPass a, CacheView c, int fmt, uint32_t gq, uint32_t gk)
+__global__ void __launch_bounds__(kThreads) qk_pass_kernel(QkPass a, CacheView c, int fmt, uint32_t gq, uint32_t gk, uint32_t first)
 {
-    uint32_t group = blockIdx.x;
+    uint32_t group = first + blockIdx.x;
     const int kind = group < gq ? 0 : group < gq + gk ? 1 : 2;
     if (kind == 1) group -= gq;
     if (kind == 2) group -= gq + gk;
@@ -206,11 +208,12 @@ slots_kernel(const int32_t* __restrict__ table, int32_t width, const int32_t* __
 // Eight features a lane, as they were written.
 template <int LPR, int FMT, typename Y>
 __global__ void __launch_bounds__(kThreads)
-read_kernel(CacheView c, const int64_t* __restrict__ slots, FastDiv heads, uint32_t rows, uint32_t gk,
+read_kernel(CacheView c, const int64_t* __restrict__ slots, FastDiv heads, uint32_t rows, uint32_t gk, uint32_t first,
             Y* __restrict__ K, Y* __restrict__ V)
 {
-    const bool value = blockIdx.x >= gk;
-    const uint32_t group = value ? blockIdx.x - gk : blockIdx.x;
+    const uint32_t at = first + blockIdx.x;
+    const bool value = at >= gk;
+    const uint32_t group = value ? at - gk : at;
     const int lane = (int)threadIdx.x % LPR;
     const uint32_t row = group * (kThreads / LPR) + threadIdx.x / LPR;
     const int b = lane >> 2, g = lane & 3;
@@ -272,6 +275,17 @@ read_kernel(CacheView c, const int64_t* __restrict__ slots, FastDiv heads, uint3
                 for (int i = 0; i < 3; ++i)
                     if (i < left) at[i] = bf16_bits(v[i]);
         }
+    }
+}
+
+// launch(the first workgroup, how many) for every piece of `groups` workgroups
+template <typename F>
+void in_pieces(uint32_t groups, F launch)
+{
+    for (uint32_t first = 0; first < groups;) {
+        const uint32_t n = groups - first < kLaunchGroups ? groups - first : kLaunchGroups;
+        launch(first, n);
+        first += n;
     }
 }
 
@@ -338,7 +352,9 @@ snack_status qk_pass(const QkPass& a, const CacheView* cache, int cache_fmt, int
             return y_fmt == SNACK_F32 ? qk_pass_kernel<LPR, EVEN, uint16_t, float> : qk_pass_kernel<LPR, EVEN, uint16_t, uint16_t>;
         };
         const auto k = even_lanes(a.d, a.ro.r) ? pick(std::true_type{}) : pick(std::false_type{});
-        hipLaunchKernelGGL(k, dim3(gq + gk + gv), dim3(kThreads), 0, s, b, c, cache_fmt, gq, gk);
+        in_pieces(gq + gk + gv, [&](uint32_t first, uint32_t n) {
+            hipLaunchKernelGGL(k, dim3(n), dim3(kThreads), 0, s, b, c, cache_fmt, gq, gk, first);
+        });
     });
     SNACK_HIP(hipGetLastError());
     return SNACK_OK;
@@ -436,12 +452,14 @@ extern "C" snack_status snack_cache_read(const snack_cache* cache, const int64_t
         constexpr int LPR = decltype(lanes)::value;
         auto launch = [&](auto fmt) {
             constexpr int FMT = decltype(fmt)::value;
-            if (y_fmt == SNACK_F32)
-                hipLaunchKernelGGL((read_kernel<LPR, FMT, float>), dim3(gk + gv), dim3(kThreads), 0, s, c, slot,
-                                   h.heads, h.rows, gk, (float*)K, (float*)V);
-            else
-                hipLaunchKernelGGL((read_kernel<LPR, FMT, uint16_t>), dim3(gk + gv), dim3(kThreads), 0, s, c, slot,
-                                   h.heads, h.rows, gk, (uint16_t*)K, (uint16_t*)V);
+            in_pieces(gk + gv, [&](uint32_t first, uint32_t n) {
+                if (y_fmt == SNACK_F32)
+                    hipLaunchKernelGGL((read_kernel<LPR, FMT, float>), dim3(n), dim3(kThreads), 0, s, c, slot, h.heads,
+                                       h.rows, gk, first, (float*)K, (float*)V);
+                else
+                    hipLaunchKernelGGL((read_kernel<LPR, FMT, uint16_t>), dim3(n), dim3(kThreads), 0, s, c, slot, h.heads,
+                                       h.rows, gk, first, (uint16_t*)K, (uint16_t*)V);
+            });
         };
         if (cache->fmt == SNACK_INT8) launch(std::integral_constant<int, SNACK_INT8>{});
         else if (cache->fmt == SNACK_E4M3) launch(std::integral_constant<int, SNACK_E4M3>{});

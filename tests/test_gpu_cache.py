@@ -200,3 +200,32 @@ def test_pages_past_2_31_bytes():
     assert (np.abs(host(out) - want) <= A.attend_tol(128, d, mag, terms, top) + 1e-37).all()
     del c
     torch.cuda.empty_cache()
+
+
+def test_past_2_32_threads():
+    """More heads than one launch takes (four lanes a head, 2^32 threads of keys and values): a few tokens written, all
+    over the call, and all of them read."""
+    import torch
+    L = lib()
+    t, h, d, page = (1 << 17) + 37, 4096, 2, 32
+    assert 2 * 4 * t * h > 2 ** 32
+    c = L.KVCache(4, h, d, A.E4M3, page=page)
+    k, v = (torch.randn(t, h, d, device="cuda", dtype=torch.bfloat16) for _ in "kv")
+    rows = torch.linspace(0, t - 1, 128, device="cuda").long()
+    slot = torch.full((t,), -1, dtype=torch.int64, device="cuda")
+    slot[rows] = torch.randperm(128, device="cuda")
+    say("past 2^32 threads: write")
+    c.write(k, v, slot)
+    few = L.KVCache(4, h, d, A.E4M3, page=page)
+    few.write(k[rows], v[rows], slot[rows])
+    assert all(torch.equal(a, b) for a, b in zip(c.read(slot[rows]), few.read(slot[rows])))
+    del k, v
+    every = torch.arange(t, device="cuda") * 5 % 128
+    say("past 2^32 threads: read")
+    gk, gv = c.read(every, torch.bfloat16)
+    wk, wv = c.read(every[:128], torch.bfloat16)
+    n = t // 128 * 128
+    assert all(torch.equal(g[:n].view(-1, 128, h, d), w.expand(n // 128, 128, h, d)) and torch.equal(g[n:], w[:t - n])
+               for g, w in ((gk, wk), (gv, wv)))
+    del gk, gv
+    torch.cuda.empty_cache()

@@ -281,3 +281,24 @@ def test_past_2_31_values():
     _close(host(dg), n * host(wg).astype(np.float64), 2 * n * chain * U32 * ag, "dgain")
     del x, dx
     torch.cuda.empty_cache()
+
+
+def test_past_2_32_threads():
+    """More heads than one launch takes (four lanes a head, 2^32 threads), against the same call in parts."""
+    import torch
+    L = lib()
+    t, h, d = (1 << 17) + 37, 8192, 2
+    assert 4 * t * h > 2 ** 32 and t * h < 2 ** 31
+    q = dev(normal((1, h, d), "rope/threads").astype(np.float32)).to(torch.bfloat16).expand(t, h, d)
+    k = dev(normal((t, 1, d), "rope/threads/k").astype(np.float32)).to(torch.bfloat16)
+    rope = L.RopeTable.make(1000, 2)
+    pos = (torch.arange(t, device="cuda") * 7 % 1000).to(torch.int32)
+    gain = torch.tensor([0.5, 1.5], device="cuda")
+    say("past 2^32 threads")
+    yq, yk = L.qk_rope_fwd(q, k, pos, rope, gain, gain)
+    step = 20011
+    for i in range(0, t, step):
+        wq, wk = L.qk_rope_fwd(q[i:i + step], k[i:i + step], pos[i:i + step], rope, gain, gain)
+        assert torch.equal(yq[i:i + step], wq) and torch.equal(yk[i:i + step], wk), i
+    del yq, wq
+    torch.cuda.empty_cache()
