@@ -310,7 +310,8 @@ snack_status check_cache(const snack_cache* c, bool bare)
         return SNACK_ERR_INVALID_ARG;
     if (!bare && (!c->data || misaligned(c->data, 16))) return SNACK_ERR_INVALID_ARG;
     // tiles are numbered in 31 bits, and bytes stay within 63: tiles < 2^31, heads < 2^13, bytes of a tile < 2^15
-    if (c->pages >= (1ll << 36) || c->pages * c->page_tokens >= (1ll << 36) || c->heads >= (1 << 13) ||
+    // (a quotient: the product of pages and tokens may pass 63 bits)
+    if (c->pages > ((1ll << 36) - 1) / c->page_tokens || c->heads >= (1 << 13) ||
         (int64_t)c->heads * c->page_tokens >= (1ll << 31))
         return SNACK_ERR_UNSUPPORTED;
     return SNACK_OK;

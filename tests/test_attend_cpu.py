@@ -217,3 +217,19 @@ def test_python_refusals():
     with pytest.raises(TypeError):
         L.KVCache(4, 2, 64, L.INT8, data=np.zeros(8))
     assert L.KVCache.nbytes_of(3, 2, 80, L.E2M1, page=32) == 3 * 2 * 32 * (2 * 48 + 3 + 4)
+
+
+def test_cache_sizes_past_63_bits():
+    """pages * page_tokens below 2^36, also where the product wraps to something small."""
+    L = _lib()
+    need = ctypes.c_int64()
+
+    def size(pages, page, **o):
+        return L._lib.snack_cache_bytes(ctypes.byref(_cache(L, pages=pages, page_tokens=page, heads=1, **o)), ctypes.byref(need))
+    for pages, page in ((1 << 34, 1 << 30), (1 << 59, 32), ((1 << 63) - 1, 32), ((1 << 62) // 32 + 1, 1 << 7), (1 << 31, 32),
+                        (1 << 6, 1 << 30)):
+        assert size(pages, page) == L.ERR_UNSUPPORTED, (pages, page)
+        with pytest.raises(L.SnackError):
+            L.KVCache.nbytes_of(pages, 1, 64, L.INT8, page=page)
+    for pages, page in (((1 << 31) - 1, 32), ((1 << 6) - 1, 1 << 30)):      # a token of 64 features: 2 (64 + 2) bytes
+        assert size(pages, page) == L.OK and need.value == pages * page * 132
