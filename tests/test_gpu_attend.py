@@ -437,3 +437,30 @@ def test_a_large_score_of_another_query_has_no_influence(fmt, nq):
             outs.append(c.run())
         assert torch.equal(outs[0][:-1], outs[1][:-1])
         assert not torch.equal(outs[0][-1], outs[1][-1])
+
+
+# query heads of a cache head, most new tokens of a sequence: blocks of 16, 64 and 256 queries (on average 2, 26, 160 of them)
+@pytest.mark.parametrize("group,most", [(1, 3), (4, 15), (32, 11)])
+def test_runs_of_sequences_and_of_blocks(group, most):
+    """More sequences, and more blocks of queries, than a workgroup has threads (512 at most): ragged, runs of them
+    without a query in the middle and at the end; then equally many queries of each, with and without starts."""
+    import torch
+    rng = np.random.default_rng(group)
+    n = 700
+    lens, nqs = rng.integers(1, 70, n), rng.integers(1, most + 1, n)
+    lens[rng.permutation(n)[:20]] = 0
+    nqs[100:180], nqs[-40:] = 0, 0
+    mean = int(nqs.sum()) * group / n
+    assert mean <= 16 if group == 1 else 16 < mean <= 128 if group == 4 else mean > 128
+    assert (nqs > 0).sum() > 512
+    c = Case(lens.tolist(), nqs.tolist(), group, 1, 32, A.INT8, 32, f"runs/{group}")
+    say("runs", group)
+    c.check(c.run())
+    nq = max(1, most // 2 + 1)
+    c.q = c.q[:nq * n] if c.q.shape[0] >= nq * n else torch.cat([c.q, c.q])[:nq * n].contiguous()
+    c.nqs, c.starts = [nq] * n, (np.arange(n + 1) * nq).astype(np.int32)
+    say("runs of equal sequences", group)
+    out = c.run()
+    c.check(out)
+    c.starts = None
+    assert torch.equal(out, c.run())
