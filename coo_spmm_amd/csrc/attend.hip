@@ -90,7 +90,8 @@ extern "C" snack_status snack_cache_attend(const snack_cache* cache, const void*
                                            int64_t work_bytes, snack_stream stream)
 {
     SNACK_CHECK(check_cache(cache, false));
-    if (q_heads < 1 || q_heads % cache->heads || width < 1 || sequences < 0 || !(scale > 0) || !isfinite(scale))
+    const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+    if (q_heads < 1 || q_heads % cache->heads || width < 1 || sequences < 0 || !(scale > 0) || !isfinite(scale_log2))
         return SNACK_ERR_INVALID_ARG;
     Heads q;
     SNACK_CHECK(make_heads(Q, q_row, q_head, q_heads, tokens, cache->head_dim, q_fmt, &q));
@@ -124,7 +125,7 @@ extern "C" snack_status snack_cache_attend(const snack_cache* cache, const void*
     a.most_blocks = (int32_t)(plan.units / cache->heads);
     a.hq = q_heads;
     a.by_group = fast_div((uint32_t)group);
-    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.causal = causal ? 1 : 0;
     a.part = (float*)work;
     a.meta = (int4*)(a.part + plan.part);

@@ -586,7 +586,7 @@ snack_status snack_cache_read(const snack_cache* cache, const int64_t* slot, int
  * A query that sees no token gets 0; tokens of no sequence are not written.  What a
  * query does not see has no influence on it, whatever it holds (NaN too).  A query
  * that would read past the table's width or a page the cache does not have gets NaN.
- * scale finite, above 0.  Sums, maxima and the softmax are held in fp32.
+ * scale above 0, scale log2(e) below 2^128.  Sums, maxima and the softmax are held in fp32.
  * SNACK_F32: q and the softmax's terms enter the products exactly, as sums of three
  * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are sums of two bf16
  * numbers (off by at most 2^-16 of themselves).

@@ -233,3 +233,16 @@ def test_cache_sizes_past_63_bits():
             L.KVCache.nbytes_of(pages, 1, 64, L.INT8, page=page)
     for pages, page in (((1 << 31) - 1, 32), ((1 << 6) - 1, 1 << 30)):      # a token of 64 features: 2 (64 + 2) bytes
         assert size(pages, page) == L.OK and need.value == pages * page * 132
+
+
+def test_largest_scale():
+    """The exponents are taken to base 2: a scale whose product with log2(e) is no fp32 number is refused (a score of 0
+    times it would be NaN); the largest other one gets as far as the workspace's check."""
+    L = _lib()
+
+    def attend(scale):
+        p = 4096
+        return L._lib.snack_cache_attend(ctypes.byref(_cache(L)), p, 128, 64, 2, L.F32, 2, p, 1, p, None, 2, scale, 1, p, p, 0, None)
+    top = float(np.finfo(np.float32).max)
+    assert attend(top) == L.ERR_INVALID_ARG and attend(top / math.log2(math.e) * (1 + 2.0 ** -20)) == L.ERR_INVALID_ARG
+    assert attend(top / math.log2(math.e) * (1 - 2.0 ** -20)) == L.ERR_WORKSPACE
