@@ -103,9 +103,19 @@ qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rota
                 ws = fma((double)wa[i], (double)x.a[i], ws);
                 ws = fma((double)wb[i], (double)x.b[i], ws);
             }
-            const double r = rsqrt64(fma(lanes_sum<LPR>(ss), inv_d, eps));
-            const float rstd = (float)r;
-            const float m = (float)(lanes_sum<LPR>(ws) * inv_d * r * r);
+            const double v = fma(lanes_sum<LPR>(ss), inv_d, eps);
+            const double r = v < __builtin_inf() ? rsqrt64(v) : v == v ? 0.0 : v;     // as the forward pass
+            // Rows about the smallest normal numbers, without eps: 1 / rms is no fp32 number.  They are taken 2^64 times as
+            // large, and their dx 2^64 times what that gives, both exact.
+            const bool tiny = r >= 0x1p126, some = __ballot(tiny) != 0;
+            const float up = tiny ? 0x1p64f : 1.0f;
+            const double rs = tiny ? r * 0x1p-64 : r;
+            if (some) {
+                x.a *= up;
+                x.b *= up;
+            }
+            const float rstd = (float)rs;
+            const float m = (float)(lanes_sum<LPR>(ws) * inv_d * r * rs);
             if (live) {
                 dg.a += dy.a * (x.a * rstd);
                 dg.b += dy.b * (x.b * rstd);
@@ -114,6 +124,10 @@ qk_bwd_kernel(BwdPart q, BwdPart k, int d, const int32_t* __restrict__ pos, Rota
             for (int i = 0; i < 4; ++i) {
                 dx.a[i] = rstd * fmaf(-x.a[i], m, wa[i]);
                 dx.b[i] = rstd * fmaf(-x.b[i], m, wb[i]);
+            }
+            if (some) {
+                dx.a *= up;
+                dx.b *= up;
             }
         }
         if (live) {

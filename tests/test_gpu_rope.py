@@ -302,3 +302,38 @@ def test_past_2_32_threads():
         assert torch.equal(yq[i:i + step], wq) and torch.equal(yk[i:i + step], wk), i
     del yq, wq
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rot", [0, 16])
+def test_backward_of_rows_whose_rms_leaves_fp32(rot):
+    """Without eps, rows down to the smallest numbers (1 / rms passes 2^128), up to the largest, between ordinary ones;
+    a gradient past fp32 is the infinity of its sign.  An infinity makes its head's dx NaN and its feature's dgain alone."""
+    import torch
+    L = lib()
+    t, h, d = 40, 2, 24
+    rng = np.random.default_rng(rot)
+    e = np.array([-149, -148, -140, -133, -129, -128, -127, -126, -125, -100, -1, 0, 60, 100, 126, 127])[np.arange(t) % 16]
+    x = np.clip(rng.standard_normal((t, h, d)), -1.9, 1.9) * np.exp2(e.astype(np.float64))[:, None, None]
+    x = x.astype(np.float32)
+    x[..., 0] = np.exp2(e.astype(np.float64)).astype(np.float32)[:, None]      # no row of zeros
+    g = (1 + 0.1 * rng.standard_normal(d)).astype(np.float32)
+    tab, pos = A.table(64, 16).astype(np.float32) if rot else None, np.arange(t) % 64
+    rope = L.RopeTable(dev(tab), A.HALF) if rot else None
+
+    def bwd(x, dy):
+        return [host(a) for a in L.qk_rope_bwd(dev(x), None, dev(pos.astype(np.int32)), dev(dy), None, rope, dev(g), eps=0.0)[::2]]
+    for size in (1.0, 2.0 ** -30, 2.0 ** -70):
+        dy = (rng.standard_normal((t, h, d)) * size).astype(np.float32)
+        say("rms", rot, size)
+        gx, gg = bwd(x, dy)
+        dx, dg, ax, ag = A.qk_bwd(x, dy, g, 0.0, tab, pos, A.HALF)
+        # as test_backward's; rstd of the largest rows is below the normal numbers, 2^-127: off by 2^-22 of itself
+        tol = 13 * U32 * ax + 2.0 ** -140
+        top = np.float64(np.finfo(np.float32).max)
+        past, near = np.abs(dx) > top + 2 * tol, np.abs(dx) > top - 2 * tol
+        assert (gx[past] == np.copysign(np.inf, dx[past])).all()
+        _close(gx[~near], dx[~near], tol[~near], "dx")
+        _close(gg, dg, (10 + 64 + 10) * U32 * ag, "dgain")
+    x[3, 1, 5] = np.inf
+    gx, gg = bwd(x, dy)
+    assert np.isnan(gx[3, 1]).all() and np.isfinite(gx[3, 0]).all() and np.isnan(gg[5]) and np.isfinite(np.delete(gg, 5)).all()
