@@ -61,7 +61,8 @@ struct AttendArgs {
     float* part;                      // two partial results a workgroup: of the block it goes on with, of the one it starts
     // What the second launch reads, two to a workgroup or (by_unit) to a unit, a block of queries of one cache head, in
     // the order of the work: of a unit that a workgroup starts and does not end {sequence's first token, block, head,
-    // pieces}, {its queries of a head, the workgroup}, else no pieces.  The last: how many units there are.
+    // pieces}, {its queries of a head, the workgroup, the last token that the sequence's first query sees}, else no
+    // pieces.  The last: how many units there are.
     int4* meta;
     int32_t by_unit;
     int32_t meta_last;
@@ -334,6 +335,13 @@ __device__ inline float max8(const float* x)
     const float a = __builtin_amdgcn_fmed3f(x[0], x[1], inf), b = __builtin_amdgcn_fmed3f(x[2], x[3], inf);
     const float c = __builtin_amdgcn_fmed3f(x[4], x[5], inf), d = __builtin_amdgcn_fmed3f(x[6], x[7], inf);
     return __builtin_amdgcn_fmed3f(__builtin_amdgcn_fmed3f(a, b, inf), __builtin_amdgcn_fmed3f(c, d, inf), inf);
+}
+
+// What a query's output is multiplied by: its last token is `limit` (below 0: it sees none, and gets 0).  A sum of 0
+// else means that all its scores are minus infinity, which have no softmax.
+__device__ inline float inverse_sum(float sum, int64_t limit)
+{
+    return sum != 0.0f ? 1.0f / sum : limit < 0 ? 0.0f : __builtin_nanf("");
 }
 
 // x as a sum of bf16 numbers, truncated one after the other (three hold all of fp32's 24 bits; the last of two
@@ -710,8 +718,8 @@ __global__ void __launch_bounds__(kAttendThreads) attend_join_kernel(AttendArgs 
     sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kStep; ++i) sum += red[i][col];
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const Row mine = get_row(a, u.z, min(row0 + col, rows - 1));
+    const float inv = inverse_sum(sum, a.causal ? u1.z + mine.i : u1.z);
     const int64_t at = ((int64_t)(u.x + mine.i) * a.hq + mine.head) * a.c.d;
     f32x4 v = {0, 0, 0, 0};
 #pragma unroll

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
         const bool whole = t0 == 0 && t1 == c.tiles;
         float* part = a.part + (int64_t)(2 * blockIdx.x + (t0 == 0 ? 1 : 0)) * part_floats(NB);
         const int64_t at = ((int64_t)(s.first + mine.i) * a.hq + mine.head) * a.c.d;
-        const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+        const float inv = whole ? inverse_sum(sum, limit) : 1.0f;
         for (int i = wave; i < 2 * NB; i += kAttendWaves) {
             f32x4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kAttendThreads, NB <= 4 ? 2 : 1) attend_kernel
             const int64_t rest = c.cost - o1;
             int4* m = a.meta + 2 * (a.by_unit ? index * a.c.heads + h : (int32_t)blockIdx.x);
             m[0] = make_int4(s.first, c.k, h, whole ? 0 : (int32_t)(1 + divide(rest + run - 1, run)));
-            m[1] = make_int4((int32_t)rows, (int32_t)blockIdx.x, 0, 0);
+            m[1] = make_int4((int32_t)rows, (int32_t)blockIdx.x, (int32_t)past, 0);
         }
         __syncthreads();
         pos += o1 - o0;
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_k
             if (whole) {
                 const Row mine = get_row(a, h, min(row[n], rows - 1));
                 const int64_t at = ((int64_t)(s.first + mine.i) * a.hq + mine.head) * a.c.d;
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                const float inv = inverse_sum(sum, limit[n]);
                 if (live)
 #pragma unroll
                     for (int i = 0; i < 2 * NB; ++i) store_out<QT>(a.out, at, 16 * i + 4 * g, a.c.d, o[n][i] * inv);
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(W * kWave, NB * NT <= 8 ? 2 : 1) attend_many_k
             const int64_t rest = c.cost - o1;
             int4* m = a.meta + 2 * (a.by_unit ? index * a.c.heads + h : (int32_t)blockIdx.x);
             m[0] = make_int4(s.first, c.k, h, whole ? 0 : (int32_t)(1 + divide(rest + run - 1, run)));
-            m[1] = make_int4((int32_t)rows, (int32_t)blockIdx.x, 0, 0);
+            m[1] = make_int4((int32_t)rows, (int32_t)blockIdx.x, (int32_t)past, 0);
         }
         pos += o1 - o0;
         o0 = 0;

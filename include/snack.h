@@ -583,10 +583,12 @@ snack_status snack_cache_read(const snack_cache* cache, const int64_t* slot, int
  *   s_t = scale q . k_t,   out = sum_t softmax(s)_t v_t
  * over the tokens t < lens[b] of its sequence, with `causal` only those up to its
  * own (t <= lens[b] - its sequence's tokens in this call + its index among them).
- * A query that sees no token gets 0; tokens of no sequence are not written.  What a
- * query does not see has no influence on it, whatever it holds (NaN too).  A query
- * that would read past the table's width or a page the cache does not have gets NaN.
- * scale above 0, scale log2(e) below 2^128.  Sums, maxima and the softmax are held in fp32.
+ * A query that sees no token gets 0, one whose scores are all minus infinity (or
+ * past fp32) NaN; tokens of no sequence are not written.  What a query does not see
+ * has no influence on it, whatever it holds (NaN too).  A query that would read past
+ * the table's width or a page the cache does not have gets NaN.
+ * scale above 0, scale log2(e) below 2^128.  Sums, maxima and the softmax are held in
+ * fp32.
  * SNACK_F32: q and the softmax's terms enter the products exactly, as sums of three
  * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are sums of two bf16
  * numbers (off by at most 2^-16 of themselves).

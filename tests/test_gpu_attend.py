@@ -493,3 +493,33 @@ def test_sequences_without_a_query_cost_little():
         times.append(sorted(spans)[len(spans) // 2])
     c.check(outs[0])
     assert torch.equal(*outs) and times[1] < 4 * times[0], times
+
+
+@pytest.mark.parametrize("n", [40, 3000])
+@pytest.mark.parametrize("nq", [1, 20, 140])
+def test_scores_that_are_all_minus_infinity(nq, n):
+    """They have no softmax: NaN, and not the 0 of a query that sees nothing; the other queries keep every bit.  Results
+    of one workgroup, and joined from many."""
+    import torch
+    for qtype in ("f32", "bf16"):
+        c = Case([n], [nq], 2, 1, 32, A.INT8, 32, f"minus/{nq}/{n}", qtype)
+        c.write(0, np.abs(normal((n, 1, 32), "minus/k")).astype(np.float32) + np.float32(0.5), normal((n, 1, 32), "minus/v").astype(np.float32))
+        clean = [c.run(False), c.run()]
+        assert all(x.isfinite().all() for x in clean)
+        for value, at in ((-np.inf, 3), (-3e38, slice(None)), (np.inf, 3), (np.nan, 3)):
+            q = c.q.clone()
+            c.q[-1, 1, at] = value
+            say("minus infinity", nq, n, qtype, value)
+            for causal in (False, True):
+                got = c.run(causal)
+                assert got[-1, 1].isnan().all()
+                got[-1, 1], want = 0, clean[causal].clone()
+                want[-1, 1] = 0
+                assert torch.equal(got, want)
+            c.q = q
+        # half of the queries before the sequence's first token: they see nothing.  (Over 40 tokens the length of 70 passes
+        # what was written: those that see past it get NaN.)
+        c.lens = [nq // 2]
+        got = host(c.run().float())
+        sees = np.arange(nq) - (nq - nq // 2)
+        assert (got[sees < 0] == 0).all() and np.isfinite(got[sees < n]).all() and np.isnan(got[sees >= n]).all()
