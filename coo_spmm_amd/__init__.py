@@ -1023,7 +1023,7 @@ class KVCache:
         """softmax(scale q . k) v over the tokens of each query's sequence, those up to its own with `causal` (else all:
         an encoder's states).  q: float32 or bfloat16 [tokens, query heads, features], each head's features contiguous,
         query heads a multiple of the cache's; scale: 1 / sqrt(features) if None.  Returns out (contiguous, of q's type
-        and shape); a query that sees no token gets 0, rows of no sequence are not written."""
+        and shape, apart from q); a query that sees no token gets 0, rows of no sequence are not written."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.attend(q, table, lens, starts, scale, causal, out)

@@ -8,7 +8,7 @@
 // bf16): each lane then holds one query throughout, its scores' maximum, sum and
 // rescaling are its own, and its probabilities are at once the second product's
 // operand.  Codes go from memory straight into operand registers (cache.h has the
-// layout); every cached value is exactly a bf16 number.  An fp32 query is split into
+// layout); a cached value is a bf16 number (steps of 2^-133).  An fp32 query is split into
 // three bf16 numbers whose sum it is, and so is every probability: three exact
 // products added in fp32, for which there is room, since the cache's bytes bound
 // this kernel.  With bf16 queries the probabilities keep 16 bits (two numbers).
@@ -21,10 +21,10 @@
 // a fixed order.
 //
 // Measured (both launches): 64 streams of 256 to 4096 tokens, 8 cache heads of 128 in
-// 4 bits, 154 MB, fp32 queries 51 us; one of 131072 tokens, 143 MB, bf16 queries 39 us
+// 4 bits, 154 MB, fp32 queries 49 us; one of 131072 tokens, 143 MB, bf16 queries 37 us
 // (a copy's rate would be 30 and 28); 512 queries over 8192 tokens, int8, 67 GFLOP,
-// bf16 (two products with V) 132 us; four prompts of 1024 tokens, 12 heads of 64, fp32 (three products
-// each) 59 us.
+// bf16 (two products with V) 132 us; four prompts of 1024 tokens, 12 heads of 64, fp32
+// (three products each) 55 us.
 #pragma once
 
 #include "cache.h"
@@ -39,7 +39,11 @@ constexpr int kAttendWaves = 4;
 constexpr int kAttendThreads = kAttendWaves * kWave;
 constexpr int kQueries = 16;          // queries of a unit
 constexpr int kAttendGroups = 512;   // workgroups at most: two a compute unit
-constexpr int kFewCost = 14, kManyCost = 4;   // what a unit costs, in tiles
+// What a unit costs, in tiles.  Measured (us, both launches): blocks of 16 queries with 4 : 14 : 28, 64 streams of 256
+// to 4096 tokens 51 : 47 : 52, 8 of 1000 17.5 : 15.6 : 15.8, one token over 16384 16.5 : 14.6 : 14.6; the others with
+// 0 : 4 : 14, 512 queries over 8192 tokens 144 : 135 : 138, four prompts of 1024 64 : 56 : 66, 64 of 64 over 200
+// 31 : 31 : 35.
+constexpr int kFewCost = 14, kManyCost = 4;
 constexpr int kMinRun = 4;            // tiles of a workgroup at least: one a wavefront
 constexpr float kRaise = 8.0f;        // a running maximum is raised when a score passes it by a factor of 2^8
 
@@ -229,8 +233,9 @@ __device__ inline Cursor find_block(const AttendArgs& a, const Schedule<THREADS>
     c.cost = c.tiles + unit_cost<ROWS>();
     return c;
 }
-// one sequence of a few blocks: every thread counts them all, without the two rounds through LDS (7.9 -> 6.5 us for
-// one token of a stream of 1000)
+// one sequence of a few blocks: every thread counts them all, without the two rounds through LDS (both launches, with
+// the rounds : without: one token of a stream of 1000 11.9 : 10.5 us, over 16384 15.9 : 14.6; up to 64 blocks instead
+// of 8 are counted no faster)
 template <int ROWS>
 __device__ inline bool few_blocks(const AttendArgs& a)
 {

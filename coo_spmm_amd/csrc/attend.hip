@@ -17,9 +17,12 @@ struct Plan {
 };
 
 // By the queries of a cache head that a sequence has on average.  Measured (us, both launches, int8, 32 query and 8
-// cache heads of 128, 8192 tokens; blocks of 16 : 64 : 256 queries): 4 sequences of 24 queries a head 37 : 32 : -, one
-// of 96 32 : 29 : 32, of 192 49 : 39 : 35, of 2048 (bf16) - : 192 : 125, (fp32) - : 278 : 249.  Blocks of 256 of heads
-// past 128 features would not fit the registers.
+// cache heads of 128, 8192 tokens; blocks of 16 : 64 : 256 queries; bf16, fp32 queries): 4 sequences of 24 queries a
+// head 39 : 38 : 59, 41 : 44 : 85; one of 96 30 : 28 : 35, 32 : 32 : 47; of 192 46 : 36 : 37, 49 : 41 : 52; of 384
+// - : 53 : 51, - : 62 : 77; of 2048 - : 185 : 133, - : 230 : 214.  (fp32 queries would have blocks of 64 up to some 500.)
+// Blocks of 256 of heads past 128 features would not fit the registers.  What is kept does not fit everywhere either:
+// fp32 heads past 96 features in blocks of 256 spill 160 bytes a lane, heads past 160 in blocks of 64 up to 660 (four
+// prompts of 2048 tokens, 8 heads, int8: of 128 features fp32 165 us, bf16 113; of 256 714 and 234).
 int attend_kind(int nb, int64_t queries)
 {
     if (queries <= kQueries) return kFew;
@@ -51,7 +54,10 @@ template <int QT, int ROWS>
 void join(const AttendArgs& a, const Plan& p, hipStream_t s)
 {
     const unsigned entries = a.by_unit ? (unsigned)p.units : p.groups;
-    if (p.units * 8 <= p.groups)     // many pieces of each
+    // Many pieces of each.  Measured (us, both launches; never : here : from two pieces on : always): one token over 131072
+    // tokens 59 : 34 : 34 : 34, eight over 16384 39 : 39 : 36 : 36, 512 queries over 8192 135 : 135 : 149 : 149, four
+    // prompts of 1024 56 : 56 : 56 : 81; from 32 pieces on 5 queries over 7 x 2000 22 against 17.
+    if (p.units * 8 <= p.groups)
         hipLaunchKernelGGL((attend_join_kernel<QT, ROWS, true>), dim3(entries, ROWS / 16, 2 * a.c.nb), dim3(kAttendThreads), 0, s, a);
     else
         hipLaunchKernelGGL((attend_join_kernel<QT, ROWS, false>), dim3(entries, ROWS / 16), dim3(kAttendThreads), 0, s, a);

@@ -91,8 +91,9 @@ __device__ inline f32x4 part4(const X* p, int left)
 }
 
 // Workgroups 0..gq-1: queries, then gk of keys, then those of values.  Measured: 8192 tokens of 32 query and 8 key heads
-// of 128, fp32 to bf16, 254 MB in 59 us (4.3 TB/s); 8192 tokens of 12 heads of 64 into an int8 cache, 126 MB in 44 us (the
-// values' codes go out two bytes at a time, into lines that eight tokens fill); one token 3.4 us (a launch).  EVEN spares
+// of 128, fp32 to bf16, 254 MB in 59 us (4.3 TB/s); 8192 tokens of 12 heads of 64 into an int8 cache, 114 MB in 44 us (the
+// values' codes go out two bytes at a time, into lines that eight tokens fill: 54 MB written for 38); one token 3.0 us
+// (a launch).  EVEN spares
 // the selects that move a partial four into place: 59 against 84 us.
 template <int LPR, bool EVEN, typename X, typename Y>
 __global__ void __launch_bounds__(kThreads) qk_pass_kernel(QkPass a, CacheView c, int fmt, uint32_t gq, uint32_t gk, uint32_t first)
@@ -205,7 +206,8 @@ slots_kernel(const int32_t* __restrict__ table, int32_t width, const int32_t* __
     slot[i] = s;
 }
 
-// Eight features a lane, as they were written.
+// Eight features a lane, as they were written.  Token by token, so a tile's lines go to many workgroups and their caches:
+// 8192 tokens of 12 heads of 64 from an int8 cache in 16 us, 50 MB fetched for the 13 that are kept.
 template <int LPR, int FMT, typename Y>
 __global__ void __launch_bounds__(kThreads)
 read_kernel(CacheView c, const int64_t* __restrict__ slots, FastDiv heads, uint32_t rows, uint32_t gk, uint32_t first,

@@ -590,8 +590,8 @@ snack_status snack_cache_read(const snack_cache* cache, const int64_t* slot, int
  * scale above 0, scale log2(e) below 2^128.  Sums, maxima and the softmax are held in
  * fp32.
  * SNACK_F32: q and the softmax's terms enter the products exactly, as sums of three
- * bf16 numbers (a cached value is one).  SNACK_BF16: the terms are sums of two bf16
- * numbers (off by at most 2^-16 of themselves).
+ * bf16 numbers (a cached value is one, down to steps of 2^-133).  SNACK_BF16: the
+ * terms are sums of two bf16 numbers (off by at most 2^-16 of themselves).
  *   work  device scratch of snack_cache_attend_work bytes, 16-byte aligned, used
  *         within the call (SNACK_ERR_WORKSPACE when work_bytes is less).
  */
